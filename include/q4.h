@@ -111,8 +111,9 @@ size_t q4_workspace_bytes(int64_t n, int64_t k, int b);
  * reused by any later call on the same stream. ws: device, 256-byte aligned. */
 q4_status q4_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
-/* Read the status header of a workspace: Q4_OK, or Q4_ERR_TIMEOUT if a bounded
- * device wait of an earlier call gave up. Synchronises the stream (the one call
+/* Read the status header of a workspace: Q4_OK, Q4_ERR_TIMEOUT if a bounded
+ * device wait of an earlier call gave up, or Q4_ERR_INVALID_ARG if q4_kv_attention
+ * met a page index outside its cache. Synchronises the stream (the one call
  * of the library that does), so call it off the hot path. */
 q4_status q4_workspace_status(const void* ws, void* stream);
 
@@ -232,6 +233,125 @@ q4_status q4_blocks_to_planes(const uint8_t* blocks, int64_t n, int64_t k, uint8
                               uint16_t* d);
 q4_status q4_planes_to_blocks(const uint8_t* qs, const uint16_t* d, int64_t n, int64_t k,
                               uint8_t* blocks);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit key/value cache and decode attention.
+ *
+ * Between the q/k/v products of a decode step and its o product stand the keys and
+ * values of every earlier token. They are held as Q4_0 blocks along the head
+ * dimension (the block, the rule of the codes and the scale are q4_pack's), 4.5 bits
+ * per value, in pages of a fixed number of tokens; a table gives each sequence its
+ * pages. "MicroLLM Lab" and "Llamas on the Web" describe no call of this kind.
+ *
+ * Layout: records of 32 tokens of one head, 36 * dim bytes each (keys, values, then
+ * both scales); record (page, head, r) starts at
+ * ((page * heads + head) * (page_size / 32) + r) * 36 * dim. With NB = dim / 32 blocks
+ * a token in chunks of C = min(NB, 4):
+ *   keys   : uint32 [NB / C][32 tokens][4][C]: word c (bytes 4c .. 4c+3) of each block
+ *   values : uint16 [NB / C][2][2][4][8][2][C]: half g (bytes 2g, 2g+1) of each block of
+ *            token 16u + 8j + 2c + e at [chunk][u][j][c][g][e][block]
+ *   scales : binary16 [32 tokens][NB] of the keys, then of the values
+ * ------------------------------------------------------------------------- */
+
+typedef enum { Q4_F32 = 0, Q4_F16 = 1, Q4_BF16 = 2 } q4_dtype;
+
+/* A cache. data: device, q4_kv_cache_bytes() bytes, 128-byte aligned, owned by the
+ * caller. heads: key/value heads, 1 .. 65535. dim: 64, 128 or 256. page_size: tokens of
+ * a page, a multiple of 32, at most 65536. pages: 1 .. 2^31 - 1. */
+typedef struct {
+    uint8_t* data;
+    int64_t pages;
+    int32_t heads;
+    int32_t dim;
+    int32_t page_size;
+} q4_kv_cache;
+
+/* Bytes to allocate for a cache; 0 for sizes that are not supported. */
+size_t q4_kv_cache_bytes(int64_t pages, int32_t heads, int32_t dim, int32_t page_size);
+
+/* A batch of sequences. All arrays are device memory, read when the kernel runs.
+ *   table    : [count][table_pages] page of each page_size tokens, rows table_stride
+ *              apart; table_pages * page_size < 2^31. An entry that is negative or not
+ *              below the cache's pages is never followed.
+ *   lens     : [count] tokens each sequence holds, its new ones included (below zero
+ *              counts as 0).
+ *   new_lens : [count] how many of a call's tokens are real, or NULL for all: token i of
+ *              sequence s has the position lens[s] - new_lens[s] + i for i < new_lens[s]
+ *              and none otherwise. Values are taken into 0 .. tokens. */
+typedef struct {
+    const int32_t* table;
+    int64_t table_stride;
+    int32_t table_pages;
+    int32_t count;
+    const int32_t* lens;
+    const int32_t* new_lens;
+} q4_kv_seqs;
+
+/* Activations [seqs][tokens][heads][dim] with strides in elements, the last dimension
+ * contiguous; data aligned to its type. Inputs may have strides of 0 (broadcast);
+ * outputs need strides of at least dim where their extent is above 1. */
+typedef struct {
+    void* data;
+    q4_dtype type;
+    int64_t seq_stride;
+    int64_t token_stride;
+    int64_t head_stride;
+} q4_rows;
+
+/* q4_kv_write - quantise new keys and values into the cache, in one launch. Tokens
+ * without a position, with a negative one, or whose page is not in the table or the
+ * cache, are skipped; nothing else of the cache changes. Codes and scales are q4_pack's
+ * of the same binary32 values, except that a block that holds a NaN or an infinity gets
+ * the scale NaN (it reads back as NaN). The positions of one call have to be distinct.
+ *   k, v : [seqs->count][tokens][cache->heads][cache->dim]
+ * tokens >= 0; no work is enqueued for zero tokens or sequences.
+ * Errors: Q4_ERR_INVALID_ARG, Q4_ERR_MISALIGNED, Q4_ERR_UNSUPPORTED (dim, type, device),
+ * Q4_ERR_CUDA. Q4_ERR_INVALID_ARG too for count * tokens * heads (twice that for dim 256) at
+ * or above 2^31. */
+q4_status q4_kv_write(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, const q4_rows* k,
+                      const q4_rows* v, void* stream);
+
+/* q4_kv_read - expand positions starts[s] .. starts[s] + tokens - 1 (starts NULL: from
+ * 0) of each sequence to dense rows, d * (q - 8) rounded once to the rows' type. Positions
+ * below 0, at or behind lens[s], or without a page give zeros. seqs->new_lens is not used.
+ * k, v, errors: as q4_kv_write (k and v are written). */
+q4_status q4_kv_read(const q4_kv_cache* cache, const q4_kv_seqs* seqs, const int32_t* starts, int32_t tokens,
+                     const q4_rows* k, const q4_rows* v, void* stream);
+
+/* What attention does to a score: x = scale * (q . k); with softcap > 0,
+ * x = softcap * tanh(x / softcap); with alibi (device, [q_heads], or NULL),
+ * x += alibi[head] * (key position - query position). With window > 0 a query at
+ * position p sees keys p - window + 1 .. p, else all of 0 .. p. scale > 0; both finite. */
+typedef struct {
+    float scale;
+    float softcap;
+    int32_t window;
+    const float* alibi;
+} q4_kv_scores;
+
+/* Workspace bytes of q4_kv_attention for a head dimension; 0 if it is not supported. The
+ * workspace is zeroed once by q4_workspace_init, may be shared with every other call of
+ * the library on the same stream, and serves one call at a time: calls that can overlap
+ * (two streams, two captured graphs replayed at once) each need their own. */
+size_t q4_kv_attention_workspace_bytes(int32_t dim);
+
+/* q4_kv_attention - softmax attention of 1 to 16 new tokens a sequence over the cache,
+ * which holds their keys and values already (q4_kv_write first, on the same stream).
+ * Query head j reads key/value head j / (q_heads / heads).
+ *   q, out : [seqs->count][tokens][q_heads][dim]; out is fully overwritten, may have
+ *            another type than q, and may not overlap it.
+ *   lse    : device, binary32 [count][tokens][q_heads], or NULL: the natural logarithm of
+ *            the sum of the exponentials of a row's scores.
+ * A query without a position, or with none that it sees, gets out = 0 and lse = -inf. Keys
+ * whose table entry is outside the cache count as masked, and the workspace's status
+ * (q4_workspace_status) becomes Q4_ERR_INVALID_ARG until it is zeroed. lens above the
+ * table's reach count as that.
+ * Scores, softmax and sums are binary32; see the kernel for what is rounded to fewer bits.
+ * Errors: as q4_kv_write, Q4_ERR_WORKSPACE, and Q4_ERR_UNSUPPORTED for tokens outside
+ * 0..16. */
+q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
+                          const q4_rows* q, const q4_kv_scores* scores, const q4_rows* out, float* lse,
+                          void* ws, size_t ws_bytes, void* stream);
 
 /* A static, human-readable name for a status code. */
 const char* q4_status_string(q4_status s);

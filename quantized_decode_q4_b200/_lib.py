@@ -42,6 +42,27 @@ class q4_stack(ctypes.Structure):
                 ("group", ctypes.POINTER(ctypes.c_int))]
 
 
+class q4_kv_cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class q4_kv_seqs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_pages", ctypes.c_int32), ("count", ctypes.c_int32),
+                ("lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p)]
+
+
+class q4_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("type", ctypes.c_int), ("seq_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class q4_kv_scores(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -54,7 +75,7 @@ def lib():
                                "`python -m quantized_decode_q4_b200.build` (nvcc, sm_100a)")
         L = ctypes.CDLL(LIB_PATH)
         c = ctypes
-        vp, i64, sz = c.c_void_p, c.c_int64, c.c_size_t
+        vp, i64, sz, i32 = c.c_void_p, c.c_int64, c.c_size_t, c.c_int32
         mp = c.POINTER(q4_matrix)
         sp = c.POINTER(q4_stack)
         sig = {
@@ -82,6 +103,12 @@ def lib():
             "q4_debug_plan_info": ([c.POINTER(i64), c.POINTER(i64), c.c_int, c.c_int,
                                     c.POINTER(i64)], c.c_int),
             "q4_debug_check_unpack": ([c.c_uint64, i64], i64),
+            # structures by address (byref, or None)
+            "q4_kv_cache_bytes": ([i64, i32, i32, i32], sz),
+            "q4_kv_write": ([vp, vp, i32, vp, vp, vp], c.c_int),
+            "q4_kv_read": ([vp, vp, vp, i32, vp, vp, vp], c.c_int),
+            "q4_kv_attention_workspace_bytes": ([i32], sz),
+            "q4_kv_attention": ([vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp], c.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -261,6 +288,194 @@ class Graph:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------------------
+# 4-bit key/value cache and attention
+# ---------------------------------------------------------------------------
+
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise Q4Error(1, what)
+
+
+class KVCache:
+    """Keys and values of many sequences as Q4_0 blocks in pages of `page_size` tokens
+    (a multiple of 32), `heads` key/value heads of `dim` values (64, 128 or 256). Owns its
+    device bytes: zeros, or `data` (uint8, contiguous, kv_cache_bytes() of it)."""
+
+    def __init__(self, pages: int, heads: int, dim: int, page_size: int = 64, device="cuda",
+                 data: torch.Tensor | None = None):
+        nbytes = kv_cache_bytes(pages, heads, dim, page_size)
+        if data is None:
+            data = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        _require(data.is_cuda and data.dtype == torch.uint8 and data.is_contiguous()
+                 and data.numel() >= nbytes, "KVCache data")
+        self.pages, self.heads, self.dim, self.page_size = pages, heads, dim, page_size
+        self.data, self.device = data, data.device
+        self.c = q4_kv_cache(data.data_ptr(), pages, heads, dim, page_size)
+
+    @property
+    def nbytes(self) -> int:
+        return self.pages * self.heads * self.page_size * self.dim * 36 // 32
+
+
+def kv_cache_bytes(pages: int, heads: int, dim: int, page_size: int) -> int:
+    # the sizes as 32-bit arguments: what does not fit is not supported either
+    fits = 0 < pages < 2**31 and all(0 < v < 2**31 for v in (heads, dim, page_size))
+    v = lib().q4_kv_cache_bytes(pages, heads, dim, page_size) if fits else 0
+    if v == 0:
+        raise Q4Error(1, "q4_kv_cache_bytes")
+    return v
+
+
+def _kv_seqs(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_lens) -> q4_kv_seqs:
+    i32, dev = torch.int32, cache.device
+    _require(table.dtype == i32 and table.dim() == 2 and table.device == dev
+             and (table.stride(1) == 1 or table.shape[1] == 1) and table.shape[1] > 0, "page table")
+    n = table.shape[0]
+    _require(lens.dtype == i32 and lens.dim() == 1 and lens.shape[0] == n and lens.device == dev
+             and lens.is_contiguous(), "lens")
+    if new_lens is not None:
+        _require(new_lens.dtype == i32 and new_lens.dim() == 1 and new_lens.shape[0] == n
+                 and new_lens.device == dev and new_lens.is_contiguous(), "new_lens")
+        new_lens = new_lens.data_ptr()
+    return q4_kv_seqs(table.data_ptr(), table.stride(0), table.shape[1], n, lens.data_ptr(), new_lens)
+
+
+def _kv_rows(cache: KVCache, t: torch.Tensor, n: int, heads: int, what: str) -> q4_rows:
+    code = _TYPES.get(t.dtype)
+    shape = t.shape
+    _require(code is not None and len(shape) == 4 and shape[0] == n and shape[2] == heads
+             and shape[3] == cache.dim and t.device == cache.device, what)
+    a, b, c, d = t.stride()
+    _require(d == 1, what)
+    return q4_rows(t.data_ptr(), code, a, b, c)
+
+
+class _On:
+    """The device of `cache` made current, and `stream` (None: the device's current one) too,
+    so that what a call allocates belongs to the stream that uses it."""
+
+    __slots__ = ("raw", "guards")
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+        for g in self.guards:
+            g.__enter__()
+        self.raw = torch._C._cuda_getCurrentRawStream(device.index)
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *e):
+        for g in reversed(self.guards):
+            g.__exit__(*e)
+
+
+def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
+             lens: torch.Tensor, new_lens: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise new keys and values [seqs][tokens][heads][dim] (binary32, binary16 or
+    bfloat16; any strides with a contiguous last dimension) into the cache. lens [seqs] counts
+    each sequence's tokens with the new ones; token i of a sequence goes to position
+    lens - new_lens + i (new_lens: all tokens if None) through table [seqs][pages]; tokens
+    without a place are skipped. The positions of a call have to be distinct."""
+    seqs = _kv_seqs(cache, table, lens, new_lens)
+    n, tokens = seqs.count, k.shape[1] if k.dim() == 4 else -1
+    ck, cv = _kv_rows(cache, k, n, cache.heads, "k"), _kv_rows(cache, v, n, cache.heads, "v")
+    _require(v.shape[1] == tokens, "k and v differ in tokens")
+    if tokens == 0 or n == 0:
+        return
+    r = ctypes.byref
+    with _On(cache.device, stream) as s:
+        _check(lib().q4_kv_write(r(cache.c), r(seqs), tokens, r(ck), r(cv), s), "q4_kv_write")
+
+
+def kv_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, tokens: int,
+            starts: torch.Tensor | None = None, dtype=torch.float32, out=None, stream=None):
+    """Keys and values of positions starts .. starts + tokens - 1 (starts [seqs], None: 0)
+    of each sequence, as a pair of [seqs][tokens][heads][dim]; zeros where a sequence holds none.
+    out: the pair to write instead of new tensors of `dtype`."""
+    seqs = _kv_seqs(cache, table, lens, None)
+    n = seqs.count
+    if starts is not None:
+        _require(starts.dtype == torch.int32 and starts.shape == lens.shape
+                 and starts.device == cache.device and starts.is_contiguous(), "starts")
+    _require(0 <= tokens < 2**31 and (out is not None or dtype in _TYPES), "tokens or dtype")
+    with _On(cache.device, stream) as s:
+        if out is None:
+            shape = (n, tokens, cache.heads, cache.dim)
+            out = (torch.empty(shape, dtype=dtype, device=cache.device),
+                   torch.empty(shape, dtype=dtype, device=cache.device))
+        k, v = out
+        ck, cv = _kv_rows(cache, k, n, cache.heads, "k"), _kv_rows(cache, v, n, cache.heads, "v")
+        _require(k.shape[1] == tokens and v.shape[1] == tokens, "tokens of the output")
+        if tokens and n:
+            r = ctypes.byref
+            _check(lib().q4_kv_read(r(cache.c), r(seqs), None if starts is None else starts.data_ptr(),
+                                    tokens, r(ck), r(cv), s), "q4_kv_read")
+    return k, v
+
+
+def kv_attention_workspace_bytes(dim: int) -> int:
+    v = lib().q4_kv_attention_workspace_bytes(dim)
+    if v == 0:
+        raise Q4Error(4, "q4_kv_attention_workspace_bytes")
+    return v
+
+
+def kv_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                 new_lens: torch.Tensor | None = None, scale: float | None = None, window: int = 0,
+                 softcap: float = 0.0, alibi: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Softmax attention of 1 to 16 new tokens a sequence, q [seqs][tokens][q_heads][dim],
+    over the cache, which holds their own keys and values already: token i stands at position
+    lens - new_lens + i and sees the positions up to its own, the last `window` of them if
+    window > 0. Scores are scale * q . k (scale: 1 / sqrt(dim) if None), capped by
+    softcap * tanh(score / softcap) if softcap > 0, plus alibi[head] * (key - query position)
+    (alibi: binary32 [q_heads]). A query that sees nothing gets 0 and lse -inf.
+    out: the result, of q's type if None; lse: binary32 [seqs][tokens][q_heads] to fill;
+    ws: a workspace of kv_attention_workspace_bytes(dim), one for each stream, else a new
+    one for this call."""
+    seqs = _kv_seqs(cache, table, lens, new_lens)
+    n = seqs.count
+    _require(q.dim() == 4, "q")
+    tokens, heads = q.shape[1], q.shape[2]
+    cq = _kv_rows(cache, q, n, heads, "q")
+    scores = q4_kv_scores(cache.dim ** -0.5 if scale is None else scale, softcap, window)
+    _require(0 <= window < 2**31, "window")
+    if alibi is not None:
+        _require(alibi.dtype == torch.float32 and alibi.shape == (heads,) and alibi.is_contiguous()
+                 and alibi.device == cache.device, "alibi")
+        scores.alibi = alibi.data_ptr()
+    if lse is not None:
+        _require(lse.dtype == torch.float32 and lse.shape == q.shape[:3] and lse.is_contiguous()
+                 and lse.device == cache.device, "lse")
+    with _On(cache.device, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
+        else:
+            _require(out.shape == q.shape, "out")
+        co = _kv_rows(cache, out, n, heads, "out")
+        if tokens == 0 or n == 0:
+            return out
+        if ws is None:
+            ws = workspace(kv_attention_workspace_bytes(cache.dim), cache.device)
+        else:
+            _require(ws.dtype == torch.uint8 and ws.device == cache.device and ws.is_contiguous(), "ws")
+        r = ctypes.byref
+        _check(lib().q4_kv_attention(r(cache.c), r(seqs), tokens, heads, r(cq), r(scores), r(co),
+                                     None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                                     ws.numel(), s), "q4_kv_attention")
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -37,6 +37,8 @@ bool cuda_failed(cudaError_t e) {
     return true;
 }
 
+void count_launches(uint64_t n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -507,7 +509,7 @@ q4_status q4_workspace_status(const void* ws, void* stream) {
     if (cuda_failed(cudaMemcpyAsync(&flag, ws, sizeof flag, cudaMemcpyDeviceToHost, st)))
         return Q4_ERR_CUDA;
     if (cuda_failed(cudaStreamSynchronize(st))) return Q4_ERR_CUDA;
-    return flag ? Q4_ERR_TIMEOUT : Q4_OK;
+    return flag & 1u ? Q4_ERR_TIMEOUT : flag ? Q4_ERR_INVALID_ARG : Q4_OK;
 }
 
 q4_status q4_gemv_batched(const q4_matrix* m, const float* X, int b, float* Y, void* ws,

@@ -45,6 +45,9 @@ struct GemvCall {
 // Record a failed CUDA call for q4_last_cuda_error() and report it.
 bool cuda_failed(cudaError_t e);
 
+// Add to q4_launch_count().
+void count_launches(uint64_t n);
+
 int64_t ceil_div(int64_t a, int64_t b);
 int64_t round_up(int64_t a, int64_t b);
 bool aligned(const void* p, uintptr_t a);

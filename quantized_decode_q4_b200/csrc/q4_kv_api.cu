@@ -1,0 +1,157 @@
+// C ABI of the 4-bit key/value cache: argument checks (before any CUDA call) and
+// launches.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/q4.h"
+#include "q4_host.h"
+#include "q4_kv_host.h"
+
+using namespace q4h;
+
+namespace {
+
+q4_status cache_size(int64_t pages, int32_t heads, int32_t dim, int32_t page_size, int64_t* bytes) {
+    if (pages < 1 || pages > INT32_MAX || heads < 1 || heads > 65535) return Q4_ERR_INVALID_ARG;
+    if (page_size < q4kv::kGroup || page_size > 65536 || page_size % q4kv::kGroup) return Q4_ERR_INVALID_ARG;
+    if (dim != 64 && dim != 128 && dim != 256) return Q4_ERR_UNSUPPORTED;
+    const int64_t page = (int64_t)heads * (page_size / q4kv::kGroup) * q4kv::record_bytes(dim);  // < 2^42
+    if (page > (INT64_C(1) << 62) / pages) return Q4_ERR_INVALID_ARG;
+    *bytes = pages * page;
+    return Q4_OK;
+}
+
+q4_status check_cache(const q4_kv_cache* c) {
+    if (!c || !c->data) return Q4_ERR_INVALID_ARG;
+    int64_t bytes = 0;
+    const q4_status s = cache_size(c->pages, c->heads, c->dim, c->page_size, &bytes);
+    if (s != Q4_OK) return s;
+    return aligned(c->data, 128) ? Q4_OK : Q4_ERR_MISALIGNED;
+}
+
+q4_status check_seqs(const q4_kv_cache* c, const q4_kv_seqs* s) {
+    if (!s || s->count < 0 || !s->table || !s->lens) return Q4_ERR_INVALID_ARG;
+    if (s->table_pages < 1 || s->table_stride < 0) return Q4_ERR_INVALID_ARG;
+    if ((int64_t)s->table_pages * c->page_size > INT32_MAX) return Q4_ERR_INVALID_ARG;
+    if (!aligned(s->table, 4) || !aligned(s->lens, 4) || !aligned(s->new_lens, 4)) return Q4_ERR_MISALIGNED;
+    return Q4_OK;
+}
+
+// Rows [seqs][tokens][heads][dim]; those that are written may not overlap.
+q4_status check_rows(const q4_rows* r, int32_t seqs, int32_t tokens, int32_t heads, int32_t dim, bool written) {
+    if (!r || !r->data) return Q4_ERR_INVALID_ARG;
+    if (r->type != Q4_F32 && r->type != Q4_F16 && r->type != Q4_BF16) return Q4_ERR_UNSUPPORTED;
+    const int64_t stride[3] = {r->seq_stride, r->token_stride, r->head_stride};
+    const int32_t extent[3] = {seqs, tokens, heads};
+    for (int i = 0; i < 3; ++i) {
+        if (stride[i] < 0 || stride[i] > (INT64_C(1) << 46)) return Q4_ERR_INVALID_ARG;
+        if (written && extent[i] > 1 && stride[i] < dim) return Q4_ERR_INVALID_ARG;
+    }
+    return aligned(r->data, r->type == Q4_F32 ? 4 : 2) ? Q4_OK : Q4_ERR_MISALIGNED;
+}
+
+q4kv::Cache cache_of(const q4_kv_cache* c) { return {c->data, c->pages, c->heads, c->page_size}; }
+
+q4kv::Seqs seqs_of(const q4_kv_seqs* s) {
+    return {s->table, s->lens, s->new_lens, s->table_stride, s->count, s->table_pages};
+}
+
+q4kv::Rows rows_of(const q4_rows* r) {
+    q4kv::Rows o = {r->data, r->seq_stride, r->token_stride, r->head_stride, (int32_t)r->type, 0};
+    const bool four = r->seq_stride % 4 == 0 && r->token_stride % 4 == 0 && r->head_stride % 4 == 0;
+    o.vec = four && aligned(r->data, r->type == Q4_F32 ? 16 : 8) ? 1 : 0;
+    return o;
+}
+
+q4_status move_call(bool write, const q4_kv_cache* cache, const q4_kv_seqs* seqs, const int32_t* starts,
+                    int32_t tokens, const q4_rows* k, const q4_rows* v, void* stream) {
+    q4_status s = check_cache(cache);
+    if (s != Q4_OK) return s;
+    if ((s = check_seqs(cache, seqs)) != Q4_OK) return s;
+    if (tokens < 0) return Q4_ERR_INVALID_ARG;
+    if ((s = check_rows(k, seqs->count, tokens, cache->heads, cache->dim, !write)) != Q4_OK) return s;
+    if ((s = check_rows(v, seqs->count, tokens, cache->heads, cache->dim, !write)) != Q4_OK) return s;
+    if (!aligned(starts, 4)) return Q4_ERR_MISALIGNED;
+    if (seqs->count == 0 || tokens == 0) return Q4_OK;
+    const int chunks = cache->dim / 32 / q4kv::chunk_blocks(cache->dim);
+    const int64_t per_token = (int64_t)cache->heads * chunks;
+    if ((int64_t)seqs->count * tokens > INT32_MAX / per_token) return Q4_ERR_INVALID_ARG;
+    int num_sms = 0;
+    if ((s = ensure_device(&num_sms)) != Q4_OK) return s;
+    q4kv::MoveParams P = {};
+    P.cache = cache_of(cache);
+    P.seqs = seqs_of(seqs);
+    P.k = rows_of(k);
+    P.v = rows_of(v);
+    P.starts = starts;
+    P.tokens = tokens;
+    P.items = (int32_t)((int64_t)seqs->count * tokens * per_token);
+    if (cuda_failed(q4kv::launch_kv_move(write, cache->dim, P, static_cast<cudaStream_t>(stream)))) return Q4_ERR_CUDA;
+    count_launches(1);
+    return Q4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t q4_kv_cache_bytes(int64_t pages, int32_t heads, int32_t dim, int32_t page_size) {
+    int64_t bytes = 0;
+    return cache_size(pages, heads, dim, page_size, &bytes) == Q4_OK ? (size_t)bytes : 0;
+}
+
+q4_status q4_kv_write(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, const q4_rows* k,
+                      const q4_rows* v, void* stream) {
+    return move_call(true, cache, seqs, nullptr, tokens, k, v, stream);
+}
+
+q4_status q4_kv_read(const q4_kv_cache* cache, const q4_kv_seqs* seqs, const int32_t* starts, int32_t tokens,
+                     const q4_rows* k, const q4_rows* v, void* stream) {
+    return move_call(false, cache, seqs, starts, tokens, k, v, stream);
+}
+
+size_t q4_kv_attention_workspace_bytes(int32_t dim) {
+    if (dim != 64 && dim != 128 && dim != 256) return 0;
+    return (size_t)kHeaderBytes;
+}
+
+q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
+                          const q4_rows* q, const q4_kv_scores* scores, const q4_rows* out, float* lse,
+                          void* ws, size_t ws_bytes, void* stream) {
+    q4_status s = check_cache(cache);
+    if (s != Q4_OK) return s;
+    if ((s = check_seqs(cache, seqs)) != Q4_OK) return s;
+    if (tokens < 0 || tokens > Q4_MAX_BATCH) return Q4_ERR_UNSUPPORTED;
+    if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads) return Q4_ERR_INVALID_ARG;
+    if (!scores || !std::isfinite(scores->scale) || !(scores->scale > 0.0f)) return Q4_ERR_INVALID_ARG;
+    if (!std::isfinite(scores->softcap) || scores->softcap < 0.0f || scores->window < 0) return Q4_ERR_INVALID_ARG;
+    if ((s = check_rows(q, seqs->count, tokens, q_heads, cache->dim, false)) != Q4_OK) return s;
+    if ((s = check_rows(out, seqs->count, tokens, q_heads, cache->dim, true)) != Q4_OK) return s;
+    if (!aligned(scores->alibi, 4) || !aligned(lse, 4)) return Q4_ERR_MISALIGNED;
+    if (!ws || ws_bytes < q4_kv_attention_workspace_bytes(cache->dim)) return Q4_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return Q4_ERR_MISALIGNED;
+    if (seqs->count == 0 || tokens == 0) return Q4_OK;
+    int num_sms = 0;
+    if ((s = ensure_device(&num_sms)) != Q4_OK) return s;
+    q4kv::AttnParams P = {};
+    P.cache = cache_of(cache);
+    P.seqs = seqs_of(seqs);
+    P.q = rows_of(q);
+    P.out = rows_of(out);
+    P.alibi = scores->alibi;
+    P.lse = lse;
+    P.ws = static_cast<uint32_t*>(ws);
+    P.scale = scores->scale;
+    P.softcap = scores->softcap;
+    P.window = scores->window;
+    P.tokens = tokens;
+    P.q_heads = q_heads;
+    if (cuda_failed(q4kv::launch_kv_attention(cache->dim, P, static_cast<cudaStream_t>(stream)))) return Q4_ERR_CUDA;
+    count_launches(1);
+    return Q4_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,102 @@
+// Layout of the 4-bit key/value cache and the arguments of its kernels, shared by
+// the kernels (q4_kv.cu, q4_kv_attn.cu), the C ABI (q4_kv_api.cu) and the host
+// replay of the layout (q4_debug.cu).
+//
+// A record holds the keys and values of 32 consecutive tokens of one head: 36 * dim
+// bytes, one bulk copy. Its codes are the 16 bytes of each Q4_0 block (byte j: code j
+// in the low nibble, code j + 16 in the high one), placed so that a lane of an
+// m16n8k16 tensor-core fragment finds its operands in one wide shared load:
+//   keys    the fragment's rows are tokens, its depth the head dimension. Lane
+//           (g, c) = (lane / 4, lane % 4) reads word c (bytes 4c .. 4c+3) of the blocks
+//           of token g: [chunk][32 tokens][4 words c][C blocks] 32-bit words.
+//   values  the rows are head dimensions, the depth tokens. Lane (g, c) reads half g
+//           (bytes 2g, 2g+1) of the blocks of tokens 8j + 2c and 8j + 2c + 1:
+//           [chunk][u][j][c][g][e][C blocks] 16-bit halves, token 16u + 8j + 2c + e.
+//   scales  binary16 [32 tokens][dim / 32] of the keys, then of the values.
+// A chunk is C = min(dim / 32, 4) blocks.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace q4kv {
+
+constexpr int kGroup = 32;           // tokens of a record
+constexpr uint32_t kBadPage = 0x100; // workspace flag: a page index outside the cache
+
+__host__ __device__ constexpr int record_bytes(int dim) { return 36 * dim; }
+__host__ __device__ constexpr int chunk_blocks(int dim) { return dim / 32 < 4 ? dim / 32 : 4; }
+
+// Byte offset in a record of 32-bit word c of key block b of token t.
+__host__ __device__ __forceinline__ int key_word(int dim, int t, int b, int c) {
+    const int cb = chunk_blocks(dim);
+    return (((b / cb * kGroup + t) * 4 + c) * cb + b % cb) * 4;
+}
+// Byte offset in a record of 16-bit half g of value block b of token t.
+__host__ __device__ __forceinline__ int value_half(int dim, int t, int b, int g) {
+    const int cb = chunk_blocks(dim);
+    const int u = t >> 4, j = (t >> 3) & 1, c = (t >> 1) & 3, e = t & 1;
+    return 16 * dim + ((((((b / cb * 2 + u) * 2 + j) * 4 + c) * 8 + g) * 2 + e) * cb + b % cb) * 2;
+}
+__host__ __device__ __forceinline__ int key_scale(int dim, int t, int b) {
+    return 32 * dim + (t * (dim / 32) + b) * 2;
+}
+__host__ __device__ __forceinline__ int value_scale(int dim, int t, int b) {
+    return 34 * dim + (t * (dim / 32) + b) * 2;
+}
+
+struct Cache {
+    uint8_t* data;
+    int64_t pages;
+    int32_t heads, page_size;
+};
+
+// Record of (page, head, position in the page).
+__host__ __device__ __forceinline__ int64_t record_at(const Cache& c, int dim, int64_t page, int head, int in_page) {
+    return ((page * c.heads + head) * (c.page_size / kGroup) + in_page / kGroup) * record_bytes(dim);
+}
+
+// The page table and the lengths of a batch of sequences.
+struct Seqs {
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* new_lens;  // nullptr: every sequence has `tokens` new ones
+    int64_t table_stride;
+    int32_t count, table_pages;
+};
+
+// Positions that the table reaches (checked on the host to fit 31 bits).
+__host__ __device__ __forceinline__ int reach(const Cache& c, const Seqs& s) { return s.table_pages * c.page_size; }
+
+__host__ __device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+struct Rows {  // [seqs][tokens][heads][dim], strides in elements
+    void* data;
+    int64_t seq, token, head;
+    int32_t type;  // q4_dtype
+    int32_t vec;   // four neighbouring elements can be moved at once
+};
+
+struct MoveParams {  // write and read
+    Cache cache;
+    Seqs seqs;
+    Rows k, v;
+    const int32_t* starts;  // read: first position of each sequence, nullptr: 0
+    int32_t tokens;
+    int32_t items;  // seqs * tokens * heads * chunks
+};
+
+struct AttnParams {
+    Cache cache;
+    Seqs seqs;
+    Rows q, out;
+    const float* alibi;  // [q_heads] or nullptr
+    float* lse;          // [seqs][tokens][q_heads] or nullptr
+    uint32_t* ws;
+    float* parts;
+    float scale, softcap;
+    int32_t tokens, q_heads, window;
+};
+
+}  // namespace q4kv

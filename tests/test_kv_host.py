@@ -1,0 +1,95 @@
+"""The 4-bit key/value cache on the CPU: sizes, refusals before any CUDA call, and the
+record layout."""
+import ctypes
+
+import pytest
+
+from quantized_decode_q4_b200 import q4
+
+INVALID, MISALIGNED, WORKSPACE, UNSUPPORTED = 1, 2, 3, 4
+
+
+def cache(data=256, pages=4, heads=2, dim=64, page=32):
+    return q4.q4_kv_cache(data, pages, heads, dim, page)
+
+
+def seqs(table=256, stride=4, pages=4, count=2, lens=256, new=None):
+    return q4.q4_kv_seqs(table, stride, pages, count, lens, new)
+
+
+def rows(data=256, type=0, s=1024, t=512, h=64):
+    return q4.q4_rows(data, type, s, t, h)
+
+
+def ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def test_cache_bytes():
+    f = q4.lib().q4_kv_cache_bytes
+    assert f(3, 5, 64, 32) == 3 * 5 * 36 * 64
+    assert f(10, 8, 128, 128) == 10 * 8 * 4 * 4608
+    assert f(2 ** 31 - 1, 65535, 256, 32) == (2 ** 31 - 1) * 65535 * 9216
+    for bad in ((0, 1, 64, 32), (-1, 1, 64, 32), (2 ** 31, 1, 64, 32), (1, 0, 64, 32), (1, 65536, 64, 32), (1, 1, 96, 32),
+                (1, 1, 0, 32), (1, 1, 64, 0), (1, 1, 64, 48), (1, 1, 64, 65568), (2 ** 31 - 1, 65535, 256, 65536)):
+        assert f(*bad) == 0, bad
+
+
+@pytest.mark.parametrize("name", ["q4_kv_write", "q4_kv_read"])
+def test_move_refusals(name):
+    L = q4.lib()
+
+    def call(c=cache(), s=seqs(), tokens=2, k=rows(), v=rows()):
+        args = (ref(c), ref(s), *([None] if name == "q4_kv_read" else []), tokens, ref(k), ref(v), None)
+        return getattr(L, name)(*args)
+
+    for c in (None, cache(data=None), cache(pages=0), cache(heads=0), cache(page=31), cache(page=48)):
+        assert call(c=c) == INVALID
+    assert call(c=cache(dim=80)) == UNSUPPORTED and call(c=cache(data=192)) == MISALIGNED
+    for s in (None, seqs(table=None), seqs(lens=None), seqs(count=-1), seqs(pages=0), seqs(stride=-1), seqs(pages=1 << 26)):
+        assert call(s=s) == INVALID
+    for s in (seqs(table=258), seqs(lens=257), seqs(new=254 + 1)):
+        assert call(s=s) == MISALIGNED
+    assert call(tokens=-1) == INVALID
+    for bad, status in ((None, INVALID), (rows(data=None), INVALID), (rows(type=3), UNSUPPORTED), (rows(type=-1), UNSUPPORTED),
+                        (rows(s=-1), INVALID), (rows(t=-64), INVALID), (rows(h=1 << 47), INVALID), (rows(data=258), MISALIGNED),
+                        (rows(data=257, type=2), MISALIGNED)):
+        assert call(k=bad) == status and call(v=bad) == status
+    # inputs may broadcast, outputs may not overlap
+    wide = rows(t=0)
+    if name == "q4_kv_read":
+        assert call(k=wide) == INVALID and call(v=rows(h=32)) == INVALID
+    assert call(s=seqs(count=1 << 20), tokens=1 << 20, k=rows(s=1 << 30, t=1024)) == INVALID
+    assert call(tokens=0) == 0 and call(s=seqs(count=0)) == 0
+
+
+def test_attention_refusals():
+    L = q4.lib()
+    need = q4.kv_attention_workspace_bytes(64)
+    assert need >= 256 and L.q4_kv_attention_workspace_bytes(96) == 0
+
+    def call(c=cache(), s=seqs(), tokens=2, heads=4, q=rows(t=256, s=512), scores=(0.125, 0.0, 0, None), out=rows(t=256, s=512), lse=None,
+             ws=256, ws_bytes=need):
+        sc = None if scores is None else q4.q4_kv_scores(*scores)
+        return L.q4_kv_attention(ref(c), ref(s), tokens, heads, ref(q), ref(sc), ref(out), lse, ws, ws_bytes, None)
+
+    assert call(tokens=0) == 0 and call(s=seqs(count=0)) == 0
+    assert call(c=None) == INVALID and call(s=None) == INVALID and call(c=cache(dim=32)) == UNSUPPORTED
+    assert call(tokens=-1) == UNSUPPORTED and call(tokens=17) == UNSUPPORTED
+    for h in (0, -2, 3, 65536):
+        assert call(heads=h) == INVALID
+    inf, nan = float("inf"), float("nan")
+    for sc in (None, (0.0, 0, 0, None), (-1.0, 0, 0, None), (nan, 0, 0, None), (inf, 0, 0, None), (1, nan, 0, None), (1, -1, 0, None),
+               (1, inf, 0, None), (1, 0, -1, None)):
+        assert call(scores=sc) == INVALID, sc
+    assert call(scores=(1, 0, 0, 258)) == MISALIGNED and call(lse=258) == MISALIGNED
+    assert call(q=None) == INVALID and call(out=None) == INVALID and call(q=rows(type=7)) == UNSUPPORTED
+    assert call(out=rows(h=0)) == INVALID and call(out=rows(t=0)) == INVALID
+    assert call(ws=None) == WORKSPACE and call(ws_bytes=need - 1) == WORKSPACE and call(ws=320) == MISALIGNED
+
+
+def test_python_sizes():
+    for bad in ((1 << 40, 1, 64, 32), (1, 1 << 32, 64, 32), (1, 1, 1 << 35, 32), (0, 1, 64, 32), (1, 1, 64, (1 << 32) + 32)):
+        with pytest.raises(q4.Q4Error):
+            q4.kv_cache_bytes(*bad)
+    assert q4.kv_cache_bytes(2, 3, 128, 64) == 2 * 3 * 2 * 4608
