@@ -85,6 +85,20 @@ int64_t q4_debug_check_tc_operands(uint64_t seed, int64_t blocks);
 q4_status q4_debug_gemv_stall(const q4_matrix* m, const float* X, int b, float* Y, void* ws,
                               size_t ws_bytes, void* stream);
 
+/* The key/value cache's record layout for a head dimension: every byte of a record
+ * belongs to exactly one code word, code half or scale, and the attention kernel's wide
+ * loads are aligned and cover the neighbours that they claim. Returns 0, or the number of
+ * the first failed check. */
+int q4_debug_check_kv_layout(int dim);
+
+/* Replay of q4_kv_attention's division of work for `count` sequences (lens, new_lens or
+ * NULL), `units` units a sequence, a table that reaches table_tokens positions, on `grid`
+ * CTAs of `warps` warps: spans cover what is seen, CTA and warp ranges cover every tile once,
+ * every unit that CTAs cut finds its partial results in distinct slots and as many
+ * arrivals as its joining CTA counts. Returns 0, or the number of the first failed check. */
+int q4_debug_check_kv_plan(const int32_t* lens, const int32_t* new_lens, int count, int tokens, int window,
+                           int table_tokens, int units, int warps, int grid);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,6 +15,7 @@
 #include "q4_device.cuh"
 #include "q4_host.h"
 #include "q4_intdot.cuh"
+#include "q4_kv_plan.h"
 #include "q4_tc_math.cuh"
 #include "q4_tc_plan.h"
 
@@ -601,6 +602,105 @@ int64_t q4_debug_check_unpack(uint64_t seed, int64_t count) {
         bad += (r.x + r.y) != want;
     }
     return bad;
+}
+
+int q4_debug_check_kv_layout(int dim) {
+    using namespace q4kv;
+    if (dim != 64 && dim != 128 && dim != 256) return 1;
+    std::vector<int> hit(record_bytes(dim), 0);
+    auto mark = [&](int at, int bytes) {
+        for (int i = 0; i < bytes; ++i) {
+            if (at < 0 || at + i >= (int)hit.size()) return false;
+            ++hit[at + i];
+        }
+        return at % bytes == 0;
+    };
+    for (int t = 0; t < kGroup; ++t)
+        for (int b = 0; b < dim / 32; ++b) {
+            for (int c = 0; c < 4; ++c)
+                if (!mark(key_word(dim, t, b, c), 4)) return 2;
+            for (int g = 0; g < 8; ++g)
+                if (!mark(value_half(dim, t, b, g), 2)) return 3;
+            if (!mark(key_scale(dim, t, b), 2) || !mark(value_scale(dim, t, b), 2)) return 4;
+        }
+    for (int h : hit)
+        if (h != 1) return 5;
+    // the wide loads of the attention kernel's lanes stay aligned and are neighbours
+    const int C = chunk_blocks(dim);
+    for (int t = 0; t < kGroup; ++t)
+        for (int ch = 0; ch < dim / 32; ch += C) {
+            for (int c = 0; c < 4; ++c) {
+                if (key_word(dim, t, ch, c) % (4 * C)) return 6;
+                for (int b = 0; b < C; ++b)
+                    if (key_word(dim, t, ch + b, c) != key_word(dim, t, ch, c) + 4 * b) return 7;
+            }
+            for (int g = 0; g < 8 && t % 2 == 0; ++g) {
+                if (value_half(dim, t, ch, g) % (4 * C)) return 8;
+                for (int e = 0; e < 2; ++e)
+                    for (int b = 0; b < C; ++b)
+                        if (value_half(dim, t + e, ch + b, g) != value_half(dim, t, ch, g) + 2 * (e * C + b)) return 9;
+            }
+        }
+    return 0;
+}
+
+int q4_debug_check_kv_plan(const int32_t* lens, const int32_t* new_lens, int count, int tokens, int window,
+                           int table_tokens, int units, int warps, int grid) {
+    using namespace q4kv;
+    if (!lens || count < 1 || tokens < 1 || units < 1 || warps < 1 || grid < 1 || grid > kMaxCtas) return 1;
+    std::vector<Span> sp(count);
+    std::vector<int64_t> before(count + 1, 0);  // tiles of one unit of every earlier sequence
+    for (int s = 0; s < count; ++s) {
+        sp[s] = span_of(lens[s], new_lens ? new_lens[s] : tokens, tokens, window, table_tokens);
+        if (sp[s].n < 1 || sp[s].tile0 < 0) return 2;
+        if (!nothing(sp[s])) {
+            // the span holds the first position that a query sees and ends with the last token's record
+            const int first = std::max(0, sp[s].len - sp[s].nl), low = window > 0 ? std::max(0, first - window + 1) : 0;
+            if (sp[s].tile0 != low / kGroup || (sp[s].tile0 + sp[s].n - 1) != (sp[s].len - 1) / kGroup) return 3;
+            if ((sp[s].tile0 + sp[s].n) * (int64_t)kGroup > ((int64_t)table_tokens + kGroup - 1) / kGroup * kGroup) return 4;
+        }
+        before[s + 1] = before[s] + sp[s].n;
+    }
+    const int64_t total = before[count] * units;
+    const int ctas = ctas_of(total, warps, grid);
+    if (ctas < 1 || ctas > grid) return 5;
+    std::vector<int> arrivals(ctas, 0), wanted(ctas, 0), slot_used(2 * ctas, 0);
+    int64_t next = 0;
+    int s = 0;  // sequence of `next`
+    for (int i = 0; i < ctas; ++i) {
+        const int64_t a = part_begin(total, ctas, i), z = part_begin(total, ctas, i + 1);
+        if (a != next || z <= a || part_of(total, ctas, a) != i || part_of(total, ctas, z - 1) != i) return 6;
+        int64_t w_next = a;
+        for (int w = 0; w < warps; ++w) {
+            const int64_t wa = a + part_begin(z - a, warps, w), wz = a + part_begin(z - a, warps, w + 1);
+            if (wa != w_next || wz < wa || wz > z) return 7;
+            w_next = wz;
+        }
+        if (w_next != z) return 8;
+        // units that the CTA's range cuts
+        for (int64_t x = a; x < z;) {
+            while (x >= before[s + 1] * units) ++s;
+            const int64_t off = x - before[s] * units, start = before[s] * units + off / sp[s].n * sp[s].n, end = start + sp[s].n;
+            if (start < a || end > z) {
+                const int slot = start > a, i0 = part_of(total, ctas, start), i1 = part_of(total, ctas, end - 1);
+                if (i0 > i || i1 < i || i0 == i1) return 9;
+                if (slot_used[2 * i + slot]++) return 10;
+                // the slot in which the joining CTA looks
+                if (slot != (i == i0 ? start > part_begin(total, ctas, i0) : 0)) return 11;
+                ++arrivals[i0];
+                if (i == i0) {
+                    if (wanted[i0]) return 12;  // one count a CTA
+                    wanted[i0] = i1 - i0 + 1;
+                }
+            }
+            x = std::min(end, z);
+        }
+        next = z;
+    }
+    if (next != total) return 13;
+    for (int i = 0; i < ctas; ++i)
+        if (arrivals[i] != wanted[i] || arrivals[i] > 255) return 14;
+    return 0;
 }
 
 }  // extern "C"

@@ -115,7 +115,7 @@ q4_status q4_kv_read(const q4_kv_cache* cache, const q4_kv_seqs* seqs, const int
 
 size_t q4_kv_attention_workspace_bytes(int32_t dim) {
     if (dim != 64 && dim != 128 && dim != 256) return 0;
-    return (size_t)kHeaderBytes;
+    return (size_t)kHeaderBytes + 4 * q4kv::kv_attention_part_floats(dim);
 }
 
 q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
@@ -144,12 +144,15 @@ q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int3
     P.alibi = scores->alibi;
     P.lse = lse;
     P.ws = static_cast<uint32_t*>(ws);
+    P.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kHeaderBytes);
     P.scale = scores->scale;
     P.softcap = scores->softcap;
     P.window = scores->window;
     P.tokens = tokens;
     P.q_heads = q_heads;
-    if (cuda_failed(q4kv::launch_kv_attention(cache->dim, P, static_cast<cudaStream_t>(stream)))) return Q4_ERR_CUDA;
+    if (cuda_failed(q4kv::launch_kv_attention(cache->dim, P, num_sms,
+                                              static_cast<cudaStream_t>(stream))))
+        return Q4_ERR_CUDA;
     count_launches(1);
     return Q4_OK;
 }

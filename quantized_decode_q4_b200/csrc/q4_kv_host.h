@@ -3,9 +3,13 @@
 
 #include <cuda_runtime.h>
 
+#include <cstddef>
+
 #include "q4_kv_layout.h"
 
 namespace q4kv {
 cudaError_t launch_kv_move(bool write, int dim, const MoveParams& P, cudaStream_t stream);
-cudaError_t launch_kv_attention(int dim, const AttnParams& P, cudaStream_t stream);
+cudaError_t setup_kv_attention();
+size_t kv_attention_part_floats(int dim);
+cudaError_t launch_kv_attention(int dim, const AttnParams& P, int num_sms, cudaStream_t stream);
 }  // namespace q4kv

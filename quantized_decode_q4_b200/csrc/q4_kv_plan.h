@@ -1,0 +1,57 @@
+// How the attention kernel divides its work, shared with the host replay (q4_debug.cu).
+//
+// A unit is the query rows of one (sequence, key/value head, row tile); its tiles are the
+// 32-token records that some row of the sequence sees (one empty tile where none does, so
+// that every output row has an owner). All tiles lie end to end, sequence by sequence and
+// unit by unit; CTAs take equal ranges of them, and so do the warps of a CTA. A warp that
+// holds all tiles of a unit writes its rows; a unit cut by warps is joined in the CTA's
+// shared memory, one cut by CTAs in the workspace by the CTA that arrives last.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "q4_kv_layout.h"
+
+namespace q4kv {
+
+constexpr int kMaxCtas = 252;  // one byte of the workspace header counts arrivals per CTA
+
+// Tiles and positions of one sequence.
+struct Span {
+    int32_t tile0, n;  // first record, records
+    int32_t len, nl;   // tokens, real new tokens
+};
+
+__host__ __device__ __forceinline__ Span span_of(int len, int nl, int tokens, int window, int reach_) {
+    Span s;
+    s.len = clamp_int(len, 0, reach_);
+    s.nl = clamp_int(nl, 0, tokens);
+    s.tile0 = 0;
+    s.n = 1;
+    if (s.len > 0 && s.nl > 0) {
+        const int first = s.len > s.nl ? s.len - s.nl : 0;  // position of the first query that has one
+        if (window > 0 && first >= window) s.tile0 = (first - window + 1) / kGroup;
+        s.n = (s.len - 1) / kGroup + 1 - s.tile0;
+    }
+    return s;
+}
+
+__host__ __device__ __forceinline__ bool nothing(const Span& s) { return s.len <= 0 || s.nl <= 0; }
+
+// CTAs that get work: at least one tile a warp.
+__host__ __device__ __forceinline__ int ctas_of(int64_t total, int warps, int grid) {
+    const int64_t want = (total + warps - 1) / warps;
+    return want < grid ? (int)want : grid;
+}
+
+// First tile of part i of `parts` equal ranges of `total` tiles.
+__host__ __device__ __forceinline__ int64_t part_begin(int64_t total, int parts, int64_t i) { return total * i / parts; }
+
+// The part that holds tile x.
+__host__ __device__ __forceinline__ int part_of(int64_t total, int parts, int64_t x) {
+    return (int)(((x + 1) * parts - 1) / total);
+}
+
+}  // namespace q4kv

@@ -2,6 +2,7 @@
 record layout."""
 import ctypes
 
+import numpy as np
 import pytest
 
 from quantized_decode_q4_b200 import q4
@@ -93,3 +94,44 @@ def test_python_sizes():
         with pytest.raises(q4.Q4Error):
             q4.kv_cache_bytes(*bad)
     assert q4.kv_cache_bytes(2, 3, 128, 64) == 2 * 3 * 2 * 4608
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_record_layout(dim):
+    f = q4.lib().q4_debug_check_kv_layout
+    f.argtypes, f.restype = [ctypes.c_int], ctypes.c_int
+    assert f(dim) == 0
+    assert f(96) != 0
+
+
+def test_attention_plans_replay_on_host():
+    """Every tile is covered once and every cut unit is joined once: one sequence and many,
+    empty ones, windows, lengths behind the table, fewer tiles than warps and far more."""
+    f = q4.lib().q4_debug_check_kv_plan
+    i32p = ctypes.POINTER(ctypes.c_int32)
+    f.argtypes, f.restype = [i32p, i32p] + [ctypes.c_int] * 7, ctypes.c_int
+    rng = np.random.default_rng(11)
+
+    def check(lens, new, tokens, window, reach, units, warps, grid):
+        n = len(lens)
+        a = (ctypes.c_int32 * n)(*lens)
+        b = None if new is None else (ctypes.c_int32 * n)(*new)
+        r = f(a, b, n, tokens, window, reach, units, warps, grid)
+        assert r == 0, (r, lens[:8], tokens, window, reach, units, warps, grid)
+
+    for warps in (8, 12, 16):
+        for grid in (148, 132, 1, 7, 252):
+            check([0], None, 1, 0, 32, 1, warps, grid)
+            check([777], None, 1, 0, 800, 3, warps, grid)
+            check([8192], None, 1, 0, 8192, 8, warps, grid)
+            check([2 ** 31 - 1], None, 16, 0, 2 ** 31 - 32, 2, warps, grid)
+            check([2 ** 31 - 1, -5, 9], [3, 9, -1], 4, 4096, 2 ** 31 - 32, 9, warps, grid)
+    for _ in range(400):
+        n = int(rng.integers(1, 200)) if rng.random() < 0.7 else int(rng.integers(500, 2000))
+        top = int(2 ** rng.uniform(0, 16))
+        lens = [int(v) for v in rng.integers(-2, top + 1, n)]
+        tokens = int(rng.integers(1, 17))
+        new = None if rng.random() < 0.5 else [int(v) for v in rng.integers(-1, 20, n)]
+        window = 0 if rng.random() < 0.5 else int(2 ** rng.uniform(0, 14))
+        reach = -(-max(1, top if rng.random() < 0.8 else top // 2) // 32) * 32
+        check(lens, new, tokens, window, reach, int(rng.integers(1, 40)), int(rng.choice([8, 12, 16])), int(rng.choice([148, 3, 252])))
