@@ -662,17 +662,19 @@ int q4_debug_check_kv_plan(const int32_t* lens, const int32_t* new_lens, int cou
         before[s + 1] = before[s] + sp[s].n;
     }
     const int64_t total = before[count] * units;
-    const int ctas = ctas_of(total, warps, grid);
+    const int ctas = ctas_of(total, units, count, warps, grid);
+    const Parts parts(total, ctas);
     if (ctas < 1 || ctas > grid) return 5;
     std::vector<int> arrivals(ctas, 0), wanted(ctas, 0), slot_used(2 * ctas, 0);
     int64_t next = 0;
     int s = 0;  // sequence of `next`
     for (int i = 0; i < ctas; ++i) {
-        const int64_t a = part_begin(total, ctas, i), z = part_begin(total, ctas, i + 1);
-        if (a != next || z <= a || part_of(total, ctas, a) != i || part_of(total, ctas, z - 1) != i) return 6;
+        const int64_t a = parts.begin(i), z = parts.begin(i + 1);
+        if (a != next || z <= a || parts.of(a) != i || parts.of(z - 1) != i) return 6;
         int64_t w_next = a;
+        const Parts wp(z - a, warps);
         for (int w = 0; w < warps; ++w) {
-            const int64_t wa = a + part_begin(z - a, warps, w), wz = a + part_begin(z - a, warps, w + 1);
+            const int64_t wa = a + wp.begin(w), wz = a + wp.begin(w + 1);
             if (wa != w_next || wz < wa || wz > z) return 7;
             w_next = wz;
         }
@@ -682,11 +684,11 @@ int q4_debug_check_kv_plan(const int32_t* lens, const int32_t* new_lens, int cou
             while (x >= before[s + 1] * units) ++s;
             const int64_t off = x - before[s] * units, start = before[s] * units + off / sp[s].n * sp[s].n, end = start + sp[s].n;
             if (start < a || end > z) {
-                const int slot = start > a, i0 = part_of(total, ctas, start), i1 = part_of(total, ctas, end - 1);
+                const int slot = start > a, i0 = parts.of(start), i1 = parts.of(end - 1);
                 if (i0 > i || i1 < i || i0 == i1) return 9;
                 if (slot_used[2 * i + slot]++) return 10;
                 // the slot in which the joining CTA looks
-                if (slot != (i == i0 ? start > part_begin(total, ctas, i0) : 0)) return 11;
+                if (slot != (i == i0 ? start > parts.begin(i0) : 0)) return 11;
                 ++arrivals[i0];
                 if (i == i0) {
                     if (wanted[i0]) return 12;  // one count a CTA

@@ -47,6 +47,7 @@ namespace {
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kTimeoutFlag = 1u;
 constexpr int kRoom = 5;  // bits that scores may rise after ref was set before it moves again
+constexpr uint32_t kOnes = 0x3c003c00u;  // binary16 (1, 1)
 constexpr int kNoWindow = INT32_MAX - 64;  // positions are above -64
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -59,8 +60,10 @@ struct Cfg {
     static constexpr int RC = NT * RPL * 4;         // query rows of a unit
     static constexpr int VPT = 2 * RPL;             // scores of a lane in 16 tokens
     static constexpr int REC = record_bytes(DIM);
-    static constexpr int STAGES = DIM == 64 ? 4 : 2;
-    static constexpr int WARPS = DIM == 256 ? 8 : (DIM == 128 && NT == 2 ? 12 : 16);
+    // warps an SM: as many as hold the row tile's operands and sums in registers without
+    // spilling (spills go through what little L1 the rings leave)
+    static constexpr int WARPS = DIM == 64 ? (NT == 1 ? 16 : 12) : DIM == 128 && NT == 1 ? 12 : 8;
+    static constexpr int STAGES = DIM == 64 ? 4 : DIM == 128 ? (NT == 1 ? 3 : 4) : 2;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int ROW = DIM + 8;             // floats of a row of a partial result in shared memory
     static constexpr int PART = RC * ROW;
@@ -99,6 +102,13 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
+// The same with depth 8.
+__device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(b0));
+}
+
 __device__ __forceinline__ uint32_t transposed(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -112,6 +122,14 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t abs_half2(uint32_t a) { return a & 0x7fff7fffu; }
+
+// The larger of each half, a NaN yielding to a number.
+__device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
+    const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
@@ -172,14 +190,19 @@ __device__ __forceinline__ RowAt row_of(const AttnParams& P, const Span& sp, int
     return r;
 }
 
-// Two neighbouring outputs of a row from its sums, and the row's lse with the first pair.
-__device__ __forceinline__ void write_pair(const AttnParams& P, int s, const RowAt& r, int x, float a, float b, float m, float l) {
-    const float inv = l == 0.0f || !r.real ? 0.0f : 1.0f / l;
-    if (!r.real) a = b = 0.0f;
-    store2(P.out, row_at(P.out, s, r.i, r.hq) + x, a * inv, b * inv);
-    if (P.lse && x == 0)
-        P.lse[((int64_t)s * P.tokens + r.i) * P.q_heads + r.hq] = l == 0.0f || !r.real ? -INFINITY : (m + log2f(l)) * kLn2;
+// Where a row's result goes and what its sums are multiplied with.
+struct RowOut {
+    int64_t at;
+    float inv;
+};
+__device__ __forceinline__ RowOut row_out(const AttnParams& P, int s, const RowAt& r, float l) {
+    return {row_at(P.out, s, r.i, r.hq), l == 0.0f || !r.real ? 0.0f : 1.0f / l};
 }
+__device__ __forceinline__ void write_lse(const AttnParams& P, int s, const RowAt& r, float m, float l) {
+    if (P.lse) P.lse[((int64_t)s * P.tokens + r.i) * P.q_heads + r.hq] = l == 0.0f || !r.real ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+// A row without a position may hold any sums.
+__device__ __forceinline__ float result(float sum, float inv) { return inv == 0.0f ? 0.0f : sum * inv; }
 
 // exp2(a - b) for a <= b, 1 where both are the same infinity.
 __device__ __forceinline__ float weight(float a, float b) { return a == b ? 1.0f : ex2(a - b); }
@@ -194,16 +217,18 @@ template <class F>
 struct Warp {
     // operands of the unit's query rows
     uint32_t qb[F::NT][F::NB][4];
-    float bias[F::NT][F::NB][2];
-    float f[F::NT][F::RPL];      // score = f * accumulator (base-2 logarithm unless F::MOD)
+    uint32_t bias[F::NT][F::NB == 8 ? 2 : 1];  // SPLIT: not used
+    float f[F::NT][F::RPL];      // base-2 score = f * what step() holds
+    float scale[F::MOD ? F::NT : 1][F::RPL];
     float slope[F::MOD ? F::NT : 1][F::RPL];
     int pos[F::NT][F::RPL];      // positions of the lane's rows
     int minpos, maxpos;          // over the unit's rows that have one
     // sums
     float o[F::NB][2][F::NT][4];
-    float ob[F::NT][4];
+    float ob[F::NT][F::NB][4];   // of the weights; SPLIT: not used
     float ref[F::NT][F::RPL], l[F::NT][F::RPL];
-    int E;                       // value scales are below 2^E
+    uint32_t top_scale;          // value scales are at most this power of two 2^E (binary16)
+    float lim;                   // 15 - E: weights are below 2^lim
 
     __device__ __forceinline__ void start() {
 #pragma unroll
@@ -211,13 +236,12 @@ struct Warp {
 #pragma unroll
             for (int b = 0; b < F::NB; ++b)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) o[b][0][nt][v] = o[b][1][nt][v] = 0.0f;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) ob[nt][v] = 0.0f;
+                for (int v = 0; v < 4; ++v) o[b][0][nt][v] = o[b][1][nt][v] = ob[nt][b][v] = 0.0f;
 #pragma unroll
             for (int r = 0; r < F::RPL; ++r) ref[nt][r] = -INFINITY, l[nt][r] = 0.0f;
         }
-        E = F::SPLIT ? -14 : 0;
+        top_scale = F::SPLIT ? 0x0400u : 0x3c00u;
+        lim = F::SPLIT ? 29.0f : 15.0f;
     }
 
     // Loads the query rows of unit u of sequence s.
@@ -258,6 +282,7 @@ struct Warp {
             // a power of two that brings the row's largest element into 2^13 .. 2^14
             const int e = top == 0.0f ? 0 : clamp_int(13 - ((int)(__float_as_uint(top) >> 23) - 127), -115, 110);
             const float up = __int_as_float((e + 127) << 23), down = __int_as_float((127 - e) << 23);
+            float off[F::NB];
 #pragma unroll
             for (int b = 0; b < F::NB; ++b) {
                 float w[8], sum = 0.0f;
@@ -267,84 +292,145 @@ struct Warp {
                     float y = __half2float(__float2half_rn(x));
                     if (F::SPLIT && (g & 1)) y = __half2float(__float2half_rn(x - y));
                     sum += y;
-                    w[j] = j < 4 ? y : y * 0.0625f;  // the codes of the upper 16 are read 16 times too large
+                    w[j] = F::SPLIT || j < 4 ? y : y * 0.0625f;  // codes in place: the upper 16 are read 16 times too large
                 }
                 qb[nt][b][0] = pack_half2(w[0], w[2]);
                 qb[nt][b][1] = pack_half2(w[4], w[6]);
                 qb[nt][b][2] = pack_half2(w[1], w[3]);
                 qb[nt][b][3] = pack_half2(w[5], w[7]);
-                sum += __shfl_xor_sync(kFull, sum, 1);
-                sum += __shfl_xor_sync(kFull, sum, 2);
-                sum *= -8.0f * 0x1p-24f;
-                bias[nt][b][0] = __shfl_sync(kFull, sum, 8 * c);
-                bias[nt][b][1] = __shfl_sync(kFull, sum, 8 * c + 4);
+                if (!F::SPLIT) {
+                    sum += __shfl_xor_sync(kFull, sum, 1);
+                    sum += __shfl_xor_sync(kFull, sum, 2);
+                    off[b] = sum * (-8.0f * 0x1p-24f);
+                }
             }
-            const float fg = (F::MOD ? P.scale : P.scale * kLog2e) * 0x1p24f * down;
+            if (!F::SPLIT) {
+                // -8 * (sum of the row over block b), two binary16 parts, by depth b and NB + b
+                // of a product with the key scales (NB 8: two products; NB 2: parts 3, 4 are 0)
+                float hi[2], lo[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float t = 0.0f;
+#pragma unroll
+                    for (int b = 0; b < F::NB; ++b)
+                        if (b == (2 * c + e) % F::NB) t = off[b];
+                    hi[e] = __half2float(__float2half_rn(t));
+                    lo[e] = t - hi[e];
+                }
+                const uint32_t h2 = pack_half2(hi[0], hi[1]), l2 = pack_half2(lo[0], lo[1]);
+                if constexpr (F::NB == 8)
+                    bias[nt][0] = h2, bias[nt][1] = l2;
+                else
+                    bias[nt][0] = 2 * c < F::NB ? h2 : 2 * c < 2 * F::NB ? l2 : 0u;
+            }
+            const float fg = P.scale * (F::SPLIT ? 1.0f : 0x1p24f) * down;
 #pragma unroll
             for (int r = 0; r < F::RPL; ++r) {
-                f[nt][r] = __shfl_sync(kFull, fg, 8 * c + 4 * r);
+                const float fr = __shfl_sync(kFull, fg, 8 * c + 4 * r);
                 const int mine = min(rt * F::RC + (nt * 4 + c) * F::RPL + r, rows - 1);
                 const RowAt ra = row_of(P, at.sp, h, group, mine);
                 pos[nt][r] = first + ra.i;
-                if (F::MOD) slope[nt][r] = P.alibi ? P.alibi[ra.hq] : 0.0f;
+                f[nt][r] = F::MOD ? kLog2e : fr * kLog2e;
+                if (F::MOD) scale[nt][r] = fr, slope[nt][r] = P.alibi ? P.alibi[ra.hq] : 0.0f;
             }
         }
     }
 
-    // Moves the references so that the tile's scores x and value scales up to the half
-    // `dmax` fit, and scales the sums with them.
-    __device__ __forceinline__ void move_refs(const float (&x)[2][F::NT][F::VPT], uint32_t dmax) {
-        dmax = __reduce_max_sync(kFull, dmax);
-        int En = E;
-        if (dmax > (uint32_t)(E + 15) << 10) En = max(E, min(16, (int)(dmax >> 10) - 14));
-        const float lim = (float)(15 - En);
+    // Scales every sum and l by 2^(old reference - new one).
+    __device__ __forceinline__ void rescale(int nt, const float (&alpha)[F::RPL]) {
+#pragma unroll
+        for (int r = 0; r < F::RPL; ++r) l[nt][r] *= alpha[r];
+#pragma unroll
+        for (int b = 0; b < F::NB; ++b)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const float a = alpha[v % F::RPL];
+                o[b][0][nt][v] *= a, o[b][1][nt][v] *= a;
+                if (!F::SPLIT) ob[nt][b][v] *= a;
+            }
+    }
+
+    // Value scales up to the binary16 `dmax` come: weights get as many bits less.
+    __device__ __forceinline__ void raise_scales(uint32_t dmax) {
+        const int E = (int)(top_scale >> 10) - 15;
+        const int En = max(E, min(16, (int)(__reduce_max_sync(kFull, dmax) >> 10) - 14));
 #pragma unroll
         for (int nt = 0; nt < F::NT; ++nt) {
             float alpha[F::RPL];
 #pragma unroll
             for (int r = 0; r < F::RPL; ++r) {
-                float m = -INFINITY;
+                alpha[r] = ex2((float)(E - En));
+                ref[nt][r] += (float)(En - E);
+            }
+            rescale(nt, alpha);
+        }
+        top_scale = (uint32_t)(En + 15) << 10;
+        lim = (float)(15 - En);
+    }
+
+    // Scores s come that the references do not hold: rows with one move up to it.
+    __device__ __forceinline__ void raise_refs(const float (&s)[F::NT][F::VPT]) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+        for (int nt = 0; nt < F::NT; ++nt) {
+            float alpha[F::RPL];
 #pragma unroll
-                    for (int v = r; v < F::VPT; v += F::RPL) m = fmaxf(m, x[u][nt][v]);
+            for (int r = 0; r < F::RPL; ++r) {
+                float m = s[nt][r] * f[nt][r];
+                m = fmaxf(m, s[nt][r + F::RPL] * f[nt][r]);
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-                const float old = ref[nt][r], moved = old + (float)(En - E);
-                ref[nt][r] = m > moved + lim ? m - (lim - (float)kRoom) : moved;
+                const float old = ref[nt][r];
+                if (m > old + lim) ref[nt][r] = m - (lim - (float)kRoom);
                 alpha[r] = weight(old, ref[nt][r]);
-                l[nt][r] *= alpha[r];
             }
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const float a = alpha[v % F::RPL];
-                ob[nt][v] *= a;
-#pragma unroll
-                for (int b = 0; b < F::NB; ++b) o[b][0][nt][v] *= a, o[b][1][nt][v] *= a;
-            }
+            rescale(nt, alpha);
         }
-        E = En;
     }
 
-    // One record of 32 tokens from position p0 on. EDGE: some (row, token) is masked.
+    // A operands of four nibbles in place, `w` shifted so that they lie in the low byte of
+    // each half: SPLIT, the exact values q - 8, else the subnormals q * 2^-24 and q * 2^-20.
+    static __device__ __forceinline__ uint32_t low(uint32_t w) {
+        if (!F::SPLIT) return w & 0x000f000fu;
+        const uint32_t t = (w & 0x000f000fu) | 0x64006400u;  // 1024 + q
+        const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&t), __floats2half2_rn(-1032.0f, -1032.0f));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    static __device__ __forceinline__ uint32_t high(uint32_t w) {
+        if (!F::SPLIT) return w & 0x00f000f0u;
+        const uint32_t t = (w & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 q
+        const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&t), __floats2half2_rn(0.0625f, 0.0625f), __floats2half2_rn(-72.0f, -72.0f));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+
+    // Sixteen tokens (u: the first or the second of a record) from position p0 on. EDGE:
+    // some (row, token) is masked.
     template <bool EDGE>
-    __device__ __forceinline__ void tile(const AttnParams& P, const uint8_t* rec, int p0, int lane, const uint32_t (&ones)[F::NB]) {
+    __device__ __forceinline__ void step(const AttnParams& P, const uint8_t* rec, int u, int p0, int lane) {
         constexpr int NB = F::NB, C = F::C, NT = F::NT, DIM = F::DIM;
         const int g = lane >> 2, c = lane & 3;
-        const int window = P.window > 0 ? P.window : kNoWindow;
         // scores
-        float x[2][NT][F::VPT];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float s[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) s[nt][v] = 0.0f;
+        float s[NT][F::VPT];
+        {
+            float t[NT][4];
             uint32_t ds[2][NB / 2];
             load_words(rec + key_scale(DIM, 16 * u + g, 0), ds[0]);
             load_words(rec + key_scale(DIM, 16 * u + g + 8, 0), ds[1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) t[nt][v] = 0.0f;
+            }
+            if constexpr (!F::SPLIT) {
+                // word c (of NB / 2, going round) of the scales of tokens g and g + 8
+                const int at = 4 * (c % (NB / 2));
+                const uint32_t a0 = *reinterpret_cast<const uint32_t*>(rec + key_scale(DIM, 16 * u + g, 0) + at);
+                const uint32_t a1 = *reinterpret_cast<const uint32_t*>(rec + key_scale(DIM, 16 * u + g + 8, 0) + at);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < (NB == 8 ? 2 : 1); ++i) mma8(t[nt], a0, a1, bias[nt][i]);
+            }
 #pragma unroll
             for (int ch = 0; ch < F::NCH; ++ch) {
                 uint32_t w[2][C];
@@ -356,222 +442,312 @@ struct Warp {
                     const float d0 = b & 1 ? half_hi(ds[0][b / 2]) : half_lo(ds[0][b / 2]);
                     const float d1 = b & 1 ? half_hi(ds[1][b / 2]) : half_lo(ds[1][b / 2]);
                     const uint32_t w0 = w[0][bb], w1 = w[1][bb], y0 = w0 >> 8, y1 = w1 >> 8;
+                    const uint32_t a[8] = {low(w0), low(w1), high(w0), high(w1), low(y0), low(y1), high(y0), high(y1)};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float a[4];
-                        mma(a, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qb[nt][b][0], qb[nt][b][1],
-                            bias[nt][b][0], bias[nt][b][1], bias[nt][b][0], bias[nt][b][1]);
-                        mma(a, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qb[nt][b][2], qb[nt][b][3],
-                            a[0], a[1], a[2], a[3]);
-                        s[nt][0] = fmaf(d0, a[0], s[nt][0]);
-                        s[nt][1] = fmaf(d0, a[1], s[nt][1]);
-                        s[nt][2] = fmaf(d1, a[2], s[nt][2]);
-                        s[nt][3] = fmaf(d1, a[3], s[nt][3]);
+                        float z[4];
+                        mma(z, a[0], a[1], a[2], a[3], qb[nt][b][0], qb[nt][b][1], 0.0f, 0.0f, 0.0f, 0.0f);
+                        mma(z, a[4], a[5], a[6], a[7], qb[nt][b][2], qb[nt][b][3], z[0], z[1], z[2], z[3]);
+                        if constexpr (F::SPLIT) {
+                            t[nt][0] = fmaf(d0, z[0] + z[1], t[nt][0]);
+                            t[nt][1] = fmaf(d1, z[2] + z[3], t[nt][1]);
+                        } else {
+                            t[nt][0] = fmaf(d0, z[0], t[nt][0]);
+                            t[nt][1] = fmaf(d0, z[1], t[nt][1]);
+                            t[nt][2] = fmaf(d1, z[2], t[nt][2]);
+                            t[nt][3] = fmaf(d1, z[3], t[nt][3]);
+                        }
                     }
                 }
             }
+            const int window = P.window > 0 ? P.window : kNoWindow;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int v = 0; v < F::VPT; ++v) {
-                    const int r = v % F::RPL, key = p0 + 16 * u + g + 8 * (v / F::RPL);
-                    float t = (F::SPLIT ? s[nt][2 * v] + s[nt][2 * v + 1] : s[nt][v]) * f[nt][r];
+                    const int r = v % F::RPL, key = p0 + g + 8 * (v / F::RPL);
+                    float x = t[nt][v];
                     if (F::MOD) {
-                        if (P.softcap > 0.0f) t = P.softcap * tanhf(t / P.softcap);
-                        t = fmaf(slope[nt][r], (float)(key - pos[nt][r]), t) * kLog2e;
+                        x *= scale[nt][r];
+                        if (P.softcap > 0.0f) x = P.softcap * tanhf(x / P.softcap);
+                        x = fmaf(slope[nt][r], (float)(key - pos[nt][r]), x);
                     }
-                    if (EDGE && (key > pos[nt][r] || key <= pos[nt][r] - window)) t = -INFINITY;
-                    x[u][nt][v] = t;
+                    if (EDGE && (key > pos[nt][r] || key <= pos[nt][r] - window)) x = -INFINITY;
+                    s[nt][v] = x;
                 }
         }
-        // does every weight fit?
-        uint32_t dmax = 0;
-        {
-            uint32_t dv[NB / 2];
-            load_words(rec + value_scale(DIM, lane, 0), dv);
-            uint32_t m = 0;
+        float y[NT][F::VPT], top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < NB / 2; ++i) m = __vmaxu2(m, dv[i] & 0x7fff7fffu);
-            dmax = max(m & 0xffffu, m >> 16);
-            if (EDGE && (p0 + lane > maxpos || p0 + lane <= minpos - window)) dmax = 0;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int v = 0; v < F::VPT; ++v) {
+                y[nt][v] = fmaf(s[nt][v], f[nt][v % F::RPL], -ref[nt][v % F::RPL]);
+                top = fmaxf(top, y[nt][v]);
+            }
+        if (__any_sync(kFull, top > lim)) {
+            raise_refs(s);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int v = 0; v < F::VPT; ++v) y[nt][v] = fmaf(s[nt][v], f[nt][v % F::RPL], -ref[nt][v % F::RPL]);
         }
-        bool high = dmax > (uint32_t)(E + 15) << 10;
-        {
-            const float lim = (float)(15 - E);
+        // weights times value scales, as B operands
+        uint32_t pb[NT][NB][2];
+        if constexpr (F::SPLIT) {
+            uint32_t dv[2][NB / 2];
+            load_words(rec + value_scale(DIM, 16 * u + g, 0), dv[0]);
+            load_words(rec + value_scale(DIM, 16 * u + g + 8, 0), dv[1]);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int v = 0; v < 2; ++v) {
+                    float p = ex2(y[nt][v]);
+                    if (EDGE && s[nt][v] == -INFINITY) p = 0.0f;
+                    l[nt][0] += p;
 #pragma unroll
-                    for (int v = 0; v < F::VPT; ++v) high |= x[u][nt][v] > ref[nt][v % F::RPL] + lim;
-        }
-        if (__any_sync(kFull, high)) move_refs(x, dmax);
-        // weights and values
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            uint32_t pb[NT][NB][2];  // B operands: weights times value scales
-            if constexpr (F::SPLIT) {
-                uint32_t dv[2][NB / 2];
-                load_words(rec + value_scale(DIM, 16 * u + g, 0), dv[0]);
-                load_words(rec + value_scale(DIM, 16 * u + g + 8, 0), dv[1]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        float p = ex2(x[u][nt][v] - ref[nt][0]);
-                        if (EDGE && x[u][nt][v] == -INFINITY) p = 0.0f;
-                        l[nt][0] += p;
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            float y = p * (b & 1 ? half_hi(dv[v][b / 2]) : half_lo(dv[v][b / 2]));
-                            if (EDGE && p == 0.0f) y = 0.0f;  // whatever the scale is
-                            const float hi = __uint_as_float(__float_as_uint(y) & 0xffffe000u);
-                            pb[nt][b][v] = transposed(pack_half2(hi, y - hi));
-                        }
+                    for (int b = 0; b < NB; ++b) {
+                        float q = p * (b & 1 ? half_hi(dv[v][b / 2]) : half_lo(dv[v][b / 2]));
+                        if (EDGE && p == 0.0f) q = 0.0f;  // whatever the scale is
+                        const float hi = __uint_as_float(__float_as_uint(q) & 0xffffe000u);
+                        pb[nt][b][v] = transposed(pack_half2(hi, q - hi));
                     }
-            } else {
-                uint32_t dv[2][2][NB / 2];  // [8 j][token 2 c + e]
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    load_words(rec + value_scale(DIM, 16 * u + 8 * j + 2 * c, 0), dv[j][0]);
-                    load_words(rec + value_scale(DIM, 16 * u + 8 * j + 2 * c + 1, 0), dv[j][1]);
                 }
+        } else {
+            uint32_t dv[2][2][NB / 2];  // [8 j][token 2 c + e]
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float p[2];
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float t = x[u][nt][2 * j + r];
-                            p[r] = ex2(t - ref[nt][r]);
-                            if (EDGE && t == -INFINITY) p[r] = 0.0f;
-                            l[nt][r] += p[r];
-                        }
-                        const uint32_t pt = transposed(pack_half2(p[0], p[1]));
-                        const uint32_t keep = EDGE ? nonzero_half2(pt) : kFull;
-#pragma unroll
-                        for (int b = 0; b < NB; ++b)
-                            pb[nt][b][j] = mul_half2(pt, __byte_perm(dv[j][0][b / 2], dv[j][1][b / 2], b & 1 ? 0x7632 : 0x5410)) & keep;
-                    }
+            for (int j = 0; j < 2; ++j) {
+                load_words(rec + value_scale(DIM, 16 * u + 8 * j + 2 * c, 0), dv[j][0]);
+                load_words(rec + value_scale(DIM, 16 * u + 8 * j + 2 * c + 1, 0), dv[j][1]);
             }
 #pragma unroll
-            for (int ch = 0; ch < F::NCH; ++ch) {
-                uint32_t w[2][C];  // token pairs 2c, 2c + 1 and 8 behind: [e][C halves]
-                load_words(rec + value_half(DIM, 16 * u + 2 * c, ch * C, g), w[0]);
-                load_words(rec + value_half(DIM, 16 * u + 8 + 2 * c, ch * C, g), w[1]);
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int bb = 0; bb < C; ++bb) {
-                    const int b = ch * C + bb;
-                    const uint32_t sel = bb & 1 ? 0x7632 : 0x5410;
-                    const uint32_t y0 = __byte_perm(w[0][bb / 2], w[0][C / 2 + bb / 2], sel), z0 = y0 >> 8;
-                    const uint32_t y1 = __byte_perm(w[1][bb / 2], w[1][C / 2 + bb / 2], sel), z1 = y1 >> 8;
+                for (int j = 0; j < 2; ++j) {
+                    float p[2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float(&a)[4] = o[b][0][nt];
-                        mma(a, y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu, y1 & 0x00f000f0u, pb[nt][b][0], pb[nt][b][1], a[0], a[1], a[2], a[3]);
-                        float(&z)[4] = o[b][1][nt];
-                        mma(z, z0 & 0x000f000fu, z0 & 0x00f000f0u, z1 & 0x000f000fu, z1 & 0x00f000f0u, pb[nt][b][0], pb[nt][b][1], z[0], z[1], z[2], z[3]);
-                        float(&n)[4] = ob[nt];
-                        mma(n, ones[b], 0u, ones[b], 0u, pb[nt][b][0], pb[nt][b][1], n[0], n[1], n[2], n[3]);
+                    for (int r = 0; r < 2; ++r) {
+                        p[r] = ex2(y[nt][2 * j + r]);
+                        if (EDGE && s[nt][2 * j + r] == -INFINITY) p[r] = 0.0f;
+                        l[nt][r] += p[r];
+                    }
+                    const uint32_t pt = transposed(pack_half2(p[0], p[1]));
+                    const uint32_t keep = EDGE ? nonzero_half2(pt) : kFull;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        pb[nt][b][j] = mul_half2(pt, __byte_perm(dv[j][0][b / 2], dv[j][1][b / 2], b & 1 ? 0x7632 : 0x5410)) & keep;
+                }
+        }
+        // values
+#pragma unroll
+        for (int ch = 0; ch < F::NCH; ++ch) {
+            uint32_t w[2][C];  // token pairs 2c, 2c + 1 and 8 behind: [e][C halves]
+            load_words(rec + value_half(DIM, 16 * u + 2 * c, ch * C, g), w[0]);
+            load_words(rec + value_half(DIM, 16 * u + 8 + 2 * c, ch * C, g), w[1]);
+#pragma unroll
+            for (int bb = 0; bb < C; ++bb) {
+                const int b = ch * C + bb;
+                const uint32_t sel = bb & 1 ? 0x7632 : 0x5410;
+                const uint32_t y0 = __byte_perm(w[0][bb / 2], w[0][C / 2 + bb / 2], sel), z0 = y0 >> 8;
+                const uint32_t y1 = __byte_perm(w[1][bb / 2], w[1][C / 2 + bb / 2], sel), z1 = y1 >> 8;
+                const uint32_t a[8] = {low(y0), high(y0), low(y1), high(y1), low(z0), high(z0), low(z1), high(z1)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float(&m)[4] = o[b][0][nt];
+                    mma(m, a[0], a[1], a[2], a[3], pb[nt][b][0], pb[nt][b][1], m[0], m[1], m[2], m[3]);
+                    float(&n)[4] = o[b][1][nt];
+                    mma(n, a[4], a[5], a[6], a[7], pb[nt][b][0], pb[nt][b][1], n[0], n[1], n[2], n[3]);
+                    if constexpr (!F::SPLIT) {
+                        float(&z)[4] = ob[nt][b];
+                        mma(z, kOnes, kOnes, kOnes, kOnes, pb[nt][b][0], pb[nt][b][1], z[0], z[1], z[2], z[3]);
                     }
                 }
             }
         }
     }
 
-    // Hands the unit's sums to `put(row of the unit, element, two neighbouring sums, ref, l)`.
-    template <class Put>
-    __device__ __forceinline__ void finish(int lane, Put put) {
+    // One record of 32 tokens from position p0 on.
+    template <bool EDGE>
+    __device__ __forceinline__ void tile(const AttnParams& P, const uint8_t* rec, int p0, int lane) {
+        const int window = P.window > 0 ? P.window : kNoWindow;
+        uint32_t dv[F::NB / 2];
+        load_words(rec + value_scale(F::DIM, lane, 0), dv);
+        uint32_t m = abs_half2(dv[0]);
+#pragma unroll
+        for (int i = 1; i < F::NB / 2; ++i) m = max_half2(m, abs_half2(dv[i]));
+        m = max(m & 0xffffu, m >> 16);
+        if (EDGE && (p0 + lane > maxpos || p0 + lane <= minpos - window)) m = 0;
+        if (__any_sync(kFull, m > top_scale)) raise_scales(m);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) step<EDGE>(P, rec, u, p0 + 16 * u, lane);
+    }
+
+    // For each row of the lane, begin(row of the unit, ref, l) and pair(what that returned,
+    // element, two neighbouring sums).
+    template <class Begin, class Pair>
+    __device__ __forceinline__ void finish(int lane, Begin begin, Pair pair) {
         const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-        for (int nt = 0; nt < F::NT; ++nt) {
-            float ls[F::RPL];
+        for (int nt = 0; nt < F::NT; ++nt)
 #pragma unroll
             for (int r = 0; r < F::RPL; ++r) {
-                ls[r] = l[nt][r];
+                float ls = l[nt][r];
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) ls[r] += __shfl_xor_sync(kFull, ls[r], off);
-            }
+                for (int off = 4; off < 32; off <<= 1) ls += __shfl_xor_sync(kFull, ls, off);
+                const auto to = begin((nt * 4 + c) * F::RPL + r, ref[nt][r], ls);
 #pragma unroll
-            for (int b = 0; b < F::NB; ++b) {
-                // the block's sum of weights lies in row b of the extra accumulator
-                float w[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) w[r] = 8.0f * __shfl_sync(kFull, ob[nt][r], 4 * b + c);
-#pragma unroll
-                for (int r = 0; r < F::RPL; ++r)
+                for (int b = 0; b < F::NB; ++b)
 #pragma unroll
                     for (int up = 0; up < 2; ++up) {
-                        const float k = up ? 0x1p20f : 0x1p24f;
                         float v[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            v[e] = fmaf(o[b][e][nt][2 * up + r], k, -w[r]);
-                            if (F::SPLIT) v[e] += fmaf(o[b][e][nt][2 * up + 1], k, -w[1]);
-                        }
-                        put((nt * 4 + c) * F::RPL + r, 32 * b + 16 * up + 2 * g, v[0], v[1], ref[nt][r], ls[r]);
+                        for (int e = 0; e < 2; ++e)
+                            v[e] = F::SPLIT ? o[b][e][nt][2 * up] + o[b][e][nt][2 * up + 1]
+                                            : fmaf(o[b][e][nt][2 * up + r], up ? 0x1p20f : 0x1p24f, -8.0f * ob[nt][b][r]);
+                        pair(to, 32 * b + 16 * up + 2 * g, v[0], v[1]);
                     }
             }
-        }
     }
 };
 
 // Issues the copies of the warp's tiles, one record at a time, STAGES ahead of their use.
 template <class F>
 struct Producer {
-    Place at;
-    int64_t left;         // tiles not yet issued
-    int page, r;          // ordinal of the page in the sequence's table, record in the page
-    int base, entry;      // lane i holds entry base + i of the table's row
+    const uint8_t* from;  // the next record
+    int run;              // records behind it in the page that the warp reads, itself included
+    int left;             // tiles not yet issued
     uint32_t filled;      // per stage: a copy was issued into it
+    bool good;            // the page exists
+    // looked at where a page or a unit ends
+    int page, base, entry;  // ordinal of the page in the sequence's table; lane i holds entry base + i
+    int unit_left;          // records of the unit behind this page
+    Place at;
 
     __device__ __forceinline__ void load_entries(const AttnParams& P, int lane) {
         base = page;
         const int i = base + lane;
         entry = i < P.seqs.table_pages ? P.seqs.table[at.s * P.seqs.table_stride + i] : -1;
     }
-    __device__ __forceinline__ void seek(const AttnParams& P, int lane) {
+    // From record r of the page on.
+    __device__ __forceinline__ void open(const AttnParams& P, int rt_count, int r, int lane) {
+        const int rpp = P.cache.page_size / kGroup;
+        const int pg = __shfl_sync(kFull, entry, page - base);
+        good = (uint32_t)pg < (uint32_t)P.cache.pages && !nothing(at.sp);
+        if (!good && !nothing(at.sp) && lane == 0) atomicOr(P.ws, kBadPage);
+        const int h = rt_count == 1 ? at.u : at.u / rt_count;
+        from = P.cache.data + (((int64_t)pg * P.cache.heads + h) * rpp + r) * F::REC;
+        run = min(rpp - r, unit_left);
+        unit_left -= run;
+    }
+    __device__ __forceinline__ void seek(const AttnParams& P, int rt_count, int lane) {
         const int rpp = P.cache.page_size / kGroup, tile = at.sp.tile0 + at.t;
         page = tile / rpp;
-        r = tile - page * rpp;
+        unit_left = at.sp.n - at.t;
         load_entries(P, lane);
+        open(P, rt_count, tile - page * rpp, lane);
+    }
+    __device__ __forceinline__ void start(const AttnParams& P, const Place& place, int tiles, int rt_count, int lane) {
+        at = place;
+        left = tiles;
+        filled = 0;
+        seek(P, rt_count, lane);
     }
     __device__ __forceinline__ void issue(const AttnParams& P, int units, int rt_count, uint8_t* slot, uint64_t* bar, int stage, int lane) {
-        if (left <= 0) return;
-        const int pg = __shfl_sync(kFull, entry, page - base);
-        const bool some = !nothing(at.sp), ok = some && pg >= 0 && pg < P.cache.pages;
-        filled = (filled & ~(1u << stage)) | ((uint32_t)ok << stage);
-        if (lane == 0) {
-            if (ok) {
-                const int64_t rec = ((int64_t)pg * P.cache.heads + at.u / rt_count) * (P.cache.page_size / kGroup) + r;
-                q4dev::mbar_arrive_expect_tx(bar, F::REC);
-                q4dev::bulk_g2s(slot, P.cache.data + rec * F::REC, F::REC, bar);
-            } else if (some) {
-                atomicOr(P.ws, kBadPage);
-            }
+        if (left == 0) {
+            filled &= ~(1u << stage);
+            return;
         }
+        filled = good ? filled | 1u << stage : filled & ~(1u << stage);
+        if (good && lane == 0) {
+            q4dev::mbar_arrive_expect_tx(bar, F::REC);
+            q4dev::bulk_g2s(slot, from, F::REC, bar);
+        }
+        from += F::REC;
         --left;
-        if (++at.t < at.sp.n) {
-            if (++r == P.cache.page_size / kGroup) {
-                r = 0;
-                ++page;
-                if (page - base == 32) load_entries(P, lane);
+        if (--run == 0 && left > 0) {
+            if (unit_left > 0) {
+                if (++page - base == 32) load_entries(P, lane);
+                open(P, rt_count, 0, lane);
+            } else {
+                at.t = 0;
+                if (++at.u == units) {
+                    at.u = 0;
+                    at.sp = span_at(P, ++at.s);
+                }
+                seek(P, rt_count, lane);
             }
-        } else if (left > 0) {
-            at.t = 0;
-            if (++at.u == units) {
-                at.u = 0;
-                at.sp = span_at(P, ++at.s);
-            }
-            seek(P, lane);
         }
     }
 };
 
+// DIM sums of a row over the lanes of a warp: lane's elements 4 lane .. or 2 lane ..
+template <int DIM>
+struct RowSum {
+    static constexpr int V = DIM == 64 ? 2 : 4, N = DIM / 32 / V;
+    float v[N][V];
+    __device__ __forceinline__ RowSum() {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i][j] = 0.0f;
+    }
+    static __device__ __forceinline__ int element(int i, int lane) { return (i * 32 + lane) * V; }
+    template <bool GLOBAL>
+    __device__ __forceinline__ void add(const float* row, float k, int lane) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float* const p = row + element(i, lane);
+            if constexpr (V == 4) {
+                const float4 t = GLOBAL ? __ldcg(reinterpret_cast<const float4*>(p)) : *reinterpret_cast<const float4*>(p);
+                v[i][0] = fmaf(t.x, k, v[i][0]), v[i][1] = fmaf(t.y, k, v[i][1]);
+                v[i][2] = fmaf(t.z, k, v[i][2]), v[i][3] = fmaf(t.w, k, v[i][3]);
+            } else {
+                const float2 t = GLOBAL ? __ldcg(reinterpret_cast<const float2*>(p)) : *reinterpret_cast<const float2*>(p);
+                v[i][0] = fmaf(t.x, k, v[i][0]), v[i][1] = fmaf(t.y, k, v[i][1]);
+            }
+        }
+    }
+    __device__ __forceinline__ void keep(float* row, int lane) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float* const p = row + element(i, lane);
+            if constexpr (V == 4)
+                *reinterpret_cast<float4*>(p) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+            else
+                *reinterpret_cast<float2*>(p) = make_float2(v[i][0], v[i][1]);
+        }
+    }
+    __device__ __forceinline__ void write(const AttnParams& P, int s, const RowAt& r, float m, float l, int lane) const {
+        const RowOut to = row_out(P, s, r, l);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t at = to.at + element(i, lane);
+            if constexpr (V == 4) {
+                const float t[4] = {result(v[i][0], to.inv), result(v[i][1], to.inv), result(v[i][2], to.inv), result(v[i][3], to.inv)};
+                store4(P.out, at, t);
+            } else {
+                store2(P.out, at, result(v[i][0], to.inv), result(v[i][1], to.inv));
+            }
+        }
+        if (lane == 0) write_lse(P, s, r, m, l);
+    }
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+    return v;
+}
+
 template <class F>
-__global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const AttnParams P) {
+__global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __grid_constant__ AttnParams P) {
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t cut_start[2];  // units that this CTA shares with others: its first, its last
+    __shared__ int cut_entry[2], joins[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float* const parts = reinterpret_cast<float*>(smem + F::OFF_PART);
     float* const ml = reinterpret_cast<float*>(smem + F::OFF_ML);  // [warp][first, last][ref, l][RC]
@@ -584,10 +760,31 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const AttnP
     const int rows = P.tokens * group, rt_count = (rows + F::RC - 1) / F::RC;
     const int units = P.cache.heads * rt_count;
 
-    // tiles before each run of `run` sequences
-    const int run = (P.seqs.count + F::THREADS - 1) / F::THREADS;
-    int64_t total;
-    {
+    if (lane == 0) {
+        for (int i = 0; i < F::STAGES; ++i) q4dev::mbar_init(bars + i, 1);
+        q4dev::mbar_fence_init();
+        ents[2 * warp].part = ents[2 * warp + 1].part = -1;
+    }
+    if (tid < 2) cut_entry[tid] = -1;
+
+    // tiles of one unit of all sequences, and of those before each run of `run` sequences
+    // (up to 32 sequences: every warp for itself, a lane a sequence)
+    const bool few = P.seqs.count <= 32;
+    const int run = few ? 1 : (P.seqs.count + F::THREADS - 1) / F::THREADS;
+    Span mine = {0, 0, 0, 0};
+    int64_t all, before = 0;  // few: tiles before the lane's sequence
+    if (few) {
+        if (lane < P.seqs.count) mine = span_at(P, lane);
+        int64_t inc = mine.n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t o = __shfl_up_sync(kFull, inc, off);
+            if (lane >= off) inc += o;
+        }
+        all = __shfl_sync(kFull, inc, 31);
+        before = inc - mine.n;
+        __syncwarp();
+    } else {
         const int64_t s0 = (int64_t)tid * run;
         int64_t sum = 0;
         for (int i = 0; i < run && s0 + i < P.seqs.count; ++i) sum += span_at(P, (int)s0 + i).n;
@@ -598,115 +795,133 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const AttnP
             if (lane >= off) inc += o;
         }
         if (lane == 31) pre[F::THREADS + warp] = inc;
-        if (lane == 0) {
-            for (int i = 0; i < F::STAGES; ++i) q4dev::mbar_init(bars + i, 1);
-            q4dev::mbar_fence_init();
-            ents[2 * warp].part = ents[2 * warp + 1].part = -1;
-        }
         __syncthreads();
-        int64_t before = 0, all = 0;
+        int64_t lower = 0;
+        all = 0;
 #pragma unroll
         for (int w = 0; w < F::WARPS; ++w) {
             const int64_t o = pre[F::THREADS + w];
-            before += w < warp ? o : 0;
+            lower += w < warp ? o : 0;
             all += o;
         }
-        pre[tid] = before + inc - sum;
-        total = all * units;
+        pre[tid] = lower + inc - sum;
         __syncthreads();
     }
-    const int ctas = ctas_of(total, F::WARPS, gridDim.x);
+    const int64_t total = all * units;
+    const int ctas = ctas_of(total, units, P.seqs.count, F::WARPS, gridDim.x);
     if ((int)blockIdx.x >= ctas) return;
-    const int64_t a = part_begin(total, ctas, blockIdx.x), z = part_begin(total, ctas, blockIdx.x + 1);
-    const int64_t wa = a + part_begin(z - a, F::WARPS, warp), wz = a + part_begin(z - a, F::WARPS, warp + 1);
+    const Parts cp(total, ctas);
+    const int64_t a = cp.begin(blockIdx.x), z = cp.begin(blockIdx.x + 1);
+    const Parts wp(z - a, F::WARPS);
+    const int64_t wa = a + wp.begin(warp);
+    int todo = (int)wp.begin(warp + 1) - (int)wp.begin(warp);
 
-    if (wa < wz) {
+    if (todo > 0) {
         // the place of tile wa
         Place at;
         int64_t start;  // first tile of the unit
         {
-            const int64_t y = wa / units;
-            int lo = 0, hi = F::THREADS;  // pre[lo] <= y < pre[hi]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (pre[mid] <= y && (int64_t)mid * run < P.seqs.count)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            at.s = lo * run;
-            int64_t rest = y - pre[lo];
-            at.sp = span_at(P, at.s);
-            while (rest >= at.sp.n) {
-                rest -= at.sp.n;
-                at.sp = span_at(P, ++at.s);
+            const int64_t y = units == 1 ? wa : quotient(wa, units);
+            int64_t rest;
+            if (few) {
+                at.s = 31 - __clz(__ballot_sync(kFull, before <= y && lane < P.seqs.count));
+                rest = y - __shfl_sync(kFull, before, at.s);
+                at.sp.tile0 = __shfl_sync(kFull, mine.tile0, at.s);
+                at.sp.n = __shfl_sync(kFull, mine.n, at.s);
+                at.sp.len = __shfl_sync(kFull, mine.len, at.s);
+                at.sp.nl = __shfl_sync(kFull, mine.nl, at.s);
+            } else {
+                int lo = 0, hi = F::THREADS;  // pre[lo] <= y < pre[hi]
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (pre[mid] <= y && (int64_t)mid * run < P.seqs.count)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                at.s = lo * run;
+                rest = y - pre[lo];
+                at.sp = span_at(P, at.s);
+                while (rest >= at.sp.n) {
+                    rest -= at.sp.n;
+                    at.sp = span_at(P, ++at.s);
+                }
             }
             const int64_t off = wa - (y - rest) * units;
-            at.u = (int)(off / at.sp.n);
+            at.u = units == 1 ? 0 : (int)quotient(off, at.sp.n);
             at.t = (int)(off - (int64_t)at.u * at.sp.n);
             start = wa - at.t;
         }
         Producer<F> prod;
-        prod.at = at;
-        prod.left = wz - wa;
-        prod.filled = 0;
-        prod.seek(P, lane);
-        __syncwarp();
+        prod.start(P, at, todo, rt_count, lane);
 #pragma unroll
         for (int i = 0; i < F::STAGES; ++i) prod.issue(P, units, rt_count, ring + i * F::REC, bars + i, i, lane);
 
-        uint32_t ones[F::NB];
-#pragma unroll
-        for (int b = 0; b < F::NB; ++b) ones[b] = (lane >> 2) == b ? 0x3c003c00u : 0u;
         Warp<F> w;
         int stage = 0;
         uint32_t phases = 0;
         bool dead = false;
-        int64_t cur = wa;
-        while (cur < wz) {
-            const int n = (int)min((int64_t)(at.sp.n - at.t), wz - cur);
-            const bool whole = n == at.sp.n;
-            w.load_queries(P, at, rt_count, group, lane);
-            w.start();
+        while (todo > 0) {
+            const int n = min(at.sp.n - at.t, todo);
+            const bool whole = n == at.sp.n, empty = nothing(at.sp);
+            if (!empty) {
+                w.load_queries(P, at, rt_count, group, lane);
+                w.start();
+            }
             const int window = P.window > 0 ? P.window : kNoWindow;
+            int p0 = (at.sp.tile0 + at.t) * kGroup;
             for (int i = 0; i < n; ++i) {
                 if (prod.filled >> stage & 1) {
                     // after a wait that gave up nothing is issued or computed any more, and the
                     // copies in flight are still waited for
-                    if (!q4dev::mbar_wait_short_bounded(bars + stage, phases >> stage & 1)) dead = true;
-                    dead = __any_sync(kFull, dead);
+                    if (!__all_sync(kFull, q4dev::mbar_wait_short_bounded(bars + stage, phases >> stage & 1))) dead = true;
                     phases ^= 1u << stage;
                     if (dead) {
-                        prod.filled &= ~(1u << stage);
+                        prod.left = 0;
                     } else {
-                        const int p0 = (at.sp.tile0 + at.t + i) * kGroup;
                         const uint8_t* rec = ring + stage * F::REC;
                         if (p0 + kGroup - 1 <= w.minpos && p0 > w.maxpos - window)
-                            w.template tile<false>(P, rec, p0, lane, ones);
+                            w.template tile<false>(P, rec, p0, lane);
                         else
-                            w.template tile<true>(P, rec, p0, lane, ones);
+                            w.template tile<true>(P, rec, p0, lane);
                     }
                 }
                 __syncwarp();
-                if (!dead) prod.issue(P, units, rt_count, ring + stage * F::REC, bars + stage, stage, lane);
+                prod.issue(P, units, rt_count, ring + stage * F::REC, bars + stage, stage, lane);
                 stage = stage + 1 == F::STAGES ? 0 : stage + 1;
+                p0 += kGroup;
             }
-            cur += n;
-            if (whole) {
-                const int h = at.u / rt_count, row0 = (at.u - h * rt_count) * F::RC;
-                w.finish(lane, [&](int row, int x, float v0, float v1, float m, float l) {
-                    if (row0 + row < rows) write_pair(P, at.s, row_of(P, at.sp, h, group, row0 + row), x, v0, v1, m, l);
-                });
+            todo -= n;
+            const int h = rt_count == 1 ? at.u : at.u / rt_count, row0 = (at.u - h * rt_count) * F::RC;
+            if (empty) {
+                for (int row = row0; row < min(row0 + F::RC, rows); ++row)
+                    RowSum<F::DIM>().write(P, at.s, row_of(P, at.sp, h, group, row), -INFINITY, 0.0f, lane);
+            } else if (whole) {
+                w.finish(
+                    lane,
+                    [&](int row, float m, float l) {
+                        const bool there = row0 + row < rows;
+                        const RowAt r = row_of(P, at.sp, h, group, there ? row0 + row : 0);
+                        RowOut to = row_out(P, at.s, r, l);
+                        if (there && lane < 4) write_lse(P, at.s, r, m, l);
+                        if (!there) to.at = -1;
+                        return to;
+                    },
+                    [&](const RowOut& to, int x, float v0, float v1) {
+                        if (to.at >= 0) store2(P.out, to.at + x, result(v0, to.inv), result(v1, to.inv));
+                    });
             } else {
                 // the ring is free once the warp's last tile is done
-                const bool last = cur == wz;
+                const bool last = todo == 0;
                 float* const p = last ? reinterpret_cast<float*>(ring) : parts + warp * F::PART;
                 float* const rl = ml + (warp * 2 + last) * 2 * F::RC;
-                __syncwarp();
-                w.finish(lane, [&](int row, int x, float v0, float v1, float m, float l) {
-                    *reinterpret_cast<float2*>(p + row * F::ROW + x) = make_float2(v0, v1);
-                    if (x == 0) rl[row] = m, rl[F::RC + row] = l;
-                });
+                w.finish(
+                    lane,
+                    [&](int row, float m, float l) {
+                        if (lane < 4) rl[row] = m, rl[F::RC + row] = l;
+                        return p + row * F::ROW;
+                    },
+                    [&](float* to, int x, float v0, float v1) { *reinterpret_cast<float2*>(to + x) = make_float2(v0, v1); });
                 if (lane == 0) {
                     Entry& e = ents[2 * warp + last];
                     e.start = start, e.s = at.s, e.u = at.u, e.n = at.sp.n;
@@ -714,7 +929,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const AttnP
                 }
             }
             start += at.sp.n;
-            if (cur < wz) {
+            if (todo > 0) {
                 at.t = 0;
                 if (++at.u == units) {
                     at.u = 0;
@@ -726,90 +941,94 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const AttnP
     }
     __syncthreads();
 
-    // join the units that warps cut
-    __shared__ int last_cta[2];
-    __shared__ int64_t cut_start[2];
-    __shared__ int cut_entry[2];
-    if (tid < 2) cut_entry[tid] = -1;
-    __syncthreads();
-    const float* const sf = reinterpret_cast<const float*>(smem);
-    for (int e0 = 0; e0 < 2 * F::WARPS;) {
-        if (ents[e0].part < 0) {
-            ++e0;
-            continue;
-        }
-        int e1 = e0 + 1;
-        while (e1 < 2 * F::WARPS && (ents[e1].part < 0 || ents[e1].start == ents[e0].start)) ++e1;
-        const Entry en = ents[e0];
-        const bool whole = en.start >= a && en.start + en.n <= z;
-        const int slot = en.start > a;
-        if (!whole && tid == 0) cut_start[slot] = en.start, cut_entry[slot] = e0;
-        float* const wp = P.parts + ((int64_t)blockIdx.x * 2 + slot) * F::WPART;
-        const int h = en.u / rt_count, row0 = (en.u - h * rt_count) * F::RC;
-        const Span sp = span_at(P, en.s);
-        for (int i = tid; i < F::RC * F::DIM / 2; i += F::THREADS) {
-            const int row = i / (F::DIM / 2), x = 2 * (i - row * (F::DIM / 2));
-            if (row0 + row >= rows) break;
-            float m = -INFINITY;
-            for (int e = e0; e < e1; ++e)
-                if (ents[e].part >= 0) m = fmaxf(m, ml[e * 2 * F::RC + row]);
-            float v0 = 0.0f, v1 = 0.0f, l = 0.0f;
-            for (int e = e0; e < e1; ++e) {
-                if (ents[e].part < 0) continue;
-                const float k = weight(ml[e * 2 * F::RC + row], m);
-                const float2 v = *reinterpret_cast<const float2*>(sf + ents[e].part + row * F::ROW + x);
-                v0 = fmaf(v.x, k, v0), v1 = fmaf(v.y, k, v1), l = fmaf(ml[e * 2 * F::RC + F::RC + row], k, l);
+    // join the units that warps cut: a warp takes a row, its lanes the parts for their
+    // weights and then the elements
+    {
+        const bool valid = lane < 2 * F::WARPS && ents[lane].part >= 0;
+        const int64_t mine_start = valid ? ents[lane].start : -1;
+        const int mine_part = valid ? ents[lane].part : 0;
+        uint32_t rest = __ballot_sync(kFull, valid);
+        int task = 0;
+        while (rest) {
+            const int e0 = __ffs(rest) - 1;
+            const Entry en = ents[e0];
+            const uint32_t run_mask = __ballot_sync(kFull, valid && mine_start == en.start);
+            rest &= ~run_mask;
+            const bool whole = en.start >= a && en.start + en.n <= z;
+            const int slot = en.start > a;
+            if (!whole && tid == 0) cut_start[slot] = en.start, cut_entry[slot] = e0;
+            const int h = rt_count == 1 ? en.u : en.u / rt_count, row0 = (en.u - h * rt_count) * F::RC;
+            const int n = min(F::RC, rows - row0);
+            for (int row = 0; row < n; ++row) {
+                if (task++ % F::WARPS != warp) continue;
+                const bool in = run_mask >> lane & 1;
+                const float m = in ? ml[lane * 2 * F::RC + row] : -INFINITY;
+                const float top = warp_max(m);
+                const float k = in ? weight(m, top) : 0.0f;
+                const float l = warp_sum(in ? k * ml[lane * 2 * F::RC + F::RC + row] : 0.0f);
+                RowSum<F::DIM> sum;
+                for (uint32_t left = run_mask; left; left &= left - 1) {
+                    const int e = __ffs(left) - 1;
+                    sum.template add<false>(reinterpret_cast<const float*>(smem) + __shfl_sync(kFull, mine_part, e) + row * F::ROW,
+                                            __shfl_sync(kFull, k, e), lane);
+                }
+                if (whole) {
+                    const Span sp = span_at(P, en.s);
+                    sum.write(P, en.s, row_of(P, sp, h, group, row0 + row), top, l, lane);
+                } else {
+                    float* const to = P.parts + ((int64_t)blockIdx.x * 2 + slot) * F::WPART;
+                    sum.keep(to + row * F::DIM, lane);
+                    if (lane == 0) to[F::RC * F::DIM + row] = top, to[F::RC * F::DIM + F::RC + row] = l;
+                }
             }
-            if (whole) {
-                write_pair(P, en.s, row_of(P, sp, h, group, row0 + row), x, v0, v1, m, l);
-            } else {
-                *reinterpret_cast<float2*>(wp + row * F::DIM + x) = make_float2(v0, v1);
-                if (x == 0) wp[F::RC * F::DIM + row] = m, wp[F::RC * F::DIM + F::RC + row] = l;
-            }
         }
-        e0 = e1;
     }
-    __threadfence();
     __syncthreads();
     // and those that CTAs cut: the last to arrive joins them in order
     if (tid < 2) {
         int join = 0;
         if (cut_entry[tid] >= 0) {
             const int64_t start = cut_start[tid];
-            const int i0 = part_of(total, ctas, start), i1 = part_of(total, ctas, start + ents[cut_entry[tid]].n - 1);
+            const int i0 = cp.of(start), i1 = cp.of(start + ents[cut_entry[tid]].n - 1);
             const int sh = 8 * (i0 & 3);
             uint32_t* const ticket = P.ws + 1 + (i0 >> 2);
+            __threadfence();
             const uint32_t old = atomicAdd(ticket, 1u << sh);
             if ((int)(old >> sh & 255u) == i1 - i0) {
                 atomicSub(ticket, (uint32_t)(i1 - i0 + 1) << sh);
+                __threadfence();
                 join = 1;
             }
         }
-        last_cta[tid] = join;
-        __threadfence();
+        joins[tid] = join;
     }
     __syncthreads();
     for (int k = 0; k < 2; ++k) {
-        if (!last_cta[k]) continue;
+        if (!joins[k]) continue;
         const Entry en = ents[cut_entry[k]];
-        const int i0 = part_of(total, ctas, en.start), i1 = part_of(total, ctas, en.start + en.n - 1);
-        const int slot0 = en.start > part_begin(total, ctas, i0);
-        const int h = en.u / rt_count, row0 = (en.u - h * rt_count) * F::RC;
+        const int i0 = cp.of(en.start), i1 = cp.of(en.start + en.n - 1);
+        const int slot0 = en.start > cp.begin(i0);
+        const int h = rt_count == 1 ? en.u : en.u / rt_count, row0 = (en.u - h * rt_count) * F::RC;
         const Span sp = span_at(P, en.s);
-        for (int i = tid; i < F::RC * F::DIM / 2; i += F::THREADS) {
-            const int row = i / (F::DIM / 2), x = 2 * (i - row * (F::DIM / 2));
-            if (row0 + row >= rows) break;
-            float m = -INFINITY;
-            for (int cta = i0; cta <= i1; ++cta)
-                m = fmaxf(m, __ldcg(P.parts + ((int64_t)cta * 2 + (cta == i0 ? slot0 : 0)) * F::WPART + F::RC * F::DIM + row));
-            float v0 = 0.0f, v1 = 0.0f, l = 0.0f;
-            for (int cta = i0; cta <= i1; ++cta) {
-                const float* const wp = P.parts + ((int64_t)cta * 2 + (cta == i0 ? slot0 : 0)) * F::WPART;
-                const float q = weight(__ldcg(wp + F::RC * F::DIM + row), m);
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(wp + row * F::DIM + x));
-                v0 = fmaf(v.x, q, v0), v1 = fmaf(v.y, q, v1), l = fmaf(__ldcg(wp + F::RC * F::DIM + F::RC + row), q, l);
+        auto part = [&](int cta) { return P.parts + ((int64_t)cta * 2 + (cta == i0 ? slot0 : 0)) * F::WPART; };
+        for (int row = warp; row < min(F::RC, rows - row0); row += F::WARPS) {
+            float top = -INFINITY, l = 0.0f;
+            for (int c0 = i0; c0 <= i1; c0 += 32)
+                if (c0 + lane <= i1) top = fmaxf(top, __ldcg(part(c0 + lane) + F::RC * F::DIM + row));
+            top = warp_max(top);
+            RowSum<F::DIM> sum;
+            for (int c0 = i0; c0 <= i1; c0 += 32) {
+                float k = 0.0f;
+                if (c0 + lane <= i1) {
+                    const float* const p = part(c0 + lane) + F::RC * F::DIM + row;
+                    k = weight(__ldcg(p), top);
+                    l = fmaf(k, __ldcg(p + F::RC), l);
+                }
+                const int n = min(32, i1 + 1 - c0);
+#pragma unroll 8
+                for (int i = 0; i < n; ++i) sum.template add<true>(part(c0 + i) + row * F::DIM, __shfl_sync(kFull, k, i), lane);
             }
-            write_pair(P, en.s, row_of(P, sp, h, group, row0 + row), x, v0, v1, m, l);
+            sum.write(P, en.s, row_of(P, sp, h, group, row0 + row), top, warp_sum(l), lane);
         }
     }
 }

@@ -40,18 +40,33 @@ __host__ __device__ __forceinline__ Span span_of(int len, int nl, int tokens, in
 
 __host__ __device__ __forceinline__ bool nothing(const Span& s) { return s.len <= 0 || s.nl <= 0; }
 
-// CTAs that get work: at least one tile a warp.
-__host__ __device__ __forceinline__ int ctas_of(int64_t total, int warps, int grid) {
-    const int64_t want = (total + warps - 1) / warps;
+// x / d, in 32 bits where both fit (a 64-bit division costs some hundred cycles).
+__host__ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t d) {
+    return ((uint64_t)x | (uint64_t)d) >> 32 ? x / d : (int64_t)((uint32_t)x / (uint32_t)d);
+}
+
+// CTAs that get work. Each warp should have at least one tile; a sequence alone whose units
+// are short takes one CTA a unit, since up to three more tiles a warp cost less than
+// joining a unit's parts through memory.
+__host__ __device__ __forceinline__ int ctas_of(int64_t total, int units, int count, int warps, int grid) {
+    if (count == 1 && units <= grid && total <= (int64_t)units * 4 * warps) return units;
+    const int64_t want = quotient(total + warps - 1, warps);
     return want < grid ? (int)want : grid;
 }
 
-// First tile of part i of `parts` equal ranges of `total` tiles.
-__host__ __device__ __forceinline__ int64_t part_begin(int64_t total, int parts, int64_t i) { return total * i / parts; }
-
-// The part that holds tile x.
-__host__ __device__ __forceinline__ int part_of(int64_t total, int parts, int64_t x) {
-    return (int)(((x + 1) * parts - 1) / total);
-}
+// `total` tiles in `parts` contiguous ranges that differ by one at most.
+struct Parts {
+    int64_t q;
+    int32_t r;
+    __host__ __device__ __forceinline__ Parts(int64_t total, int parts) {
+        q = quotient(total, parts);
+        r = (int32_t)(total - q * parts);
+    }
+    __host__ __device__ __forceinline__ int64_t begin(int i) const { return i * q + (i < r ? i : r); }
+    __host__ __device__ __forceinline__ int of(int64_t x) const {  // the range that holds tile x
+        const int64_t longer = r * (q + 1);
+        return x < longer ? (int)quotient(x, q + 1) : (int)(r + quotient(x - longer, q));
+    }
+};
 
 }  // namespace q4kv
