@@ -315,7 +315,7 @@ class KVCache:
         _require(data.is_cuda and data.dtype == torch.uint8 and data.is_contiguous()
                  and data.numel() >= nbytes, "KVCache data")
         self.pages, self.heads, self.dim, self.page_size = pages, heads, dim, page_size
-        self.data, self.device = data, data.device
+        self.data, self.device, self.index = data, data.device, data.device.index
         self.c = q4_kv_cache(data.data_ptr(), pages, heads, dim, page_size)
 
     @property
@@ -332,52 +332,48 @@ def kv_cache_bytes(pages: int, heads: int, dim: int, page_size: int) -> int:
     return v
 
 
+# The calls below take a few microseconds on the GPU, so their checks are kept to what a
+# wrong argument could not do without, in few Python operations.
+
 def _kv_seqs(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_lens) -> q4_kv_seqs:
     i32, dev = torch.int32, cache.device
-    _require(table.dtype == i32 and table.dim() == 2 and table.device == dev
-             and (table.stride(1) == 1 or table.shape[1] == 1) and table.shape[1] > 0, "page table")
-    n = table.shape[0]
-    _require(lens.dtype == i32 and lens.dim() == 1 and lens.shape[0] == n and lens.device == dev
-             and lens.is_contiguous(), "lens")
+    shape, stride = table.shape, table.stride()
+    if (len(shape) != 2 or table.dtype is not i32 or table.device != dev or shape[1] == 0
+            or (stride[1] != 1 and shape[1] != 1)):
+        raise Q4Error(1, "page table")
+    n = shape[0]
+    if lens.dtype is not i32 or lens.shape != (n,) or lens.device != dev or not lens.is_contiguous():
+        raise Q4Error(1, "lens")
     if new_lens is not None:
-        _require(new_lens.dtype == i32 and new_lens.dim() == 1 and new_lens.shape[0] == n
-                 and new_lens.device == dev and new_lens.is_contiguous(), "new_lens")
+        if (new_lens.dtype is not i32 or new_lens.shape != (n,) or new_lens.device != dev
+                or not new_lens.is_contiguous()):
+            raise Q4Error(1, "new_lens")
         new_lens = new_lens.data_ptr()
-    return q4_kv_seqs(table.data_ptr(), table.stride(0), table.shape[1], n, lens.data_ptr(), new_lens)
+    return q4_kv_seqs(table.data_ptr(), stride[0], shape[1], n, lens.data_ptr(), new_lens)
 
 
-def _kv_rows(cache: KVCache, t: torch.Tensor, n: int, heads: int, what: str) -> q4_rows:
+def _kv_rows(cache: KVCache, t: torch.Tensor, shape: tuple, what: str) -> q4_rows:
+    """The rows `t` of the given [seqs][tokens][heads][dim]."""
     code = _TYPES.get(t.dtype)
-    shape = t.shape
-    _require(code is not None and len(shape) == 4 and shape[0] == n and shape[2] == heads
-             and shape[3] == cache.dim and t.device == cache.device, what)
+    if code is None or t.shape != shape or t.device != cache.device:
+        raise Q4Error(1, what)
     a, b, c, d = t.stride()
-    _require(d == 1, what)
+    if d != 1:
+        raise Q4Error(1, what)
     return q4_rows(t.data_ptr(), code, a, b, c)
 
 
-class _On:
-    """The device of `cache` made current, and `stream` (None: the device's current one) too,
-    so that what a call allocates belongs to the stream that uses it."""
+def _elsewhere(cache: KVCache, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or torch._C._cuda_getDevice() != cache.index
 
-    __slots__ = ("raw", "guards")
 
-    def __init__(self, device, stream):
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
-        for g in self.guards:
-            g.__enter__()
-        self.raw = torch._C._cuda_getCurrentRawStream(device.index)
-
-    def __enter__(self):
-        return self.raw
-
-    def __exit__(self, *e):
-        for g in reversed(self.guards):
-            g.__exit__(*e)
+def _there(cache: KVCache, stream, call):
+    """call() with the cache's device and `stream` (None: the device's current one) current, so
+    that what it allocates belongs to the stream that uses it."""
+    _require(stream is None or stream.device == cache.device, "stream of another device")
+    with torch.cuda.device(cache.device), torch.cuda.stream(stream):
+        return call()
 
 
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
@@ -387,15 +383,19 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tens
     each sequence's tokens with the new ones; token i of a sequence goes to position
     lens - new_lens + i (new_lens: all tokens if None) through table [seqs][pages]; tokens
     without a place are skipped. The positions of a call have to be distinct."""
+    if _elsewhere(cache, stream):
+        return _there(cache, stream, lambda: kv_write(cache, k, v, table, lens, new_lens))
     seqs = _kv_seqs(cache, table, lens, new_lens)
-    n, tokens = seqs.count, k.shape[1] if k.dim() == 4 else -1
-    ck, cv = _kv_rows(cache, k, n, cache.heads, "k"), _kv_rows(cache, v, n, cache.heads, "v")
-    _require(v.shape[1] == tokens, "k and v differ in tokens")
+    n, tokens = seqs.count, k.shape[1] if k.dim() == 4 else 0
+    shape = (n, tokens, cache.heads, cache.dim)
+    ck, cv = _kv_rows(cache, k, shape, "k"), _kv_rows(cache, v, shape, "v")
     if tokens == 0 or n == 0:
         return
     r = ctypes.byref
-    with _On(cache.device, stream) as s:
-        _check(lib().q4_kv_write(r(cache.c), r(seqs), tokens, r(ck), r(cv), s), "q4_kv_write")
+    status = lib().q4_kv_write(r(cache.c), r(seqs), tokens, r(ck), r(cv),
+                               torch._C._cuda_getCurrentRawStream(cache.index))
+    if status:
+        _check(status, "q4_kv_write")
 
 
 def kv_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, tokens: int,
@@ -403,24 +403,27 @@ def kv_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, tokens: int
     """Keys and values of positions starts .. starts + tokens - 1 (starts [seqs], None: 0)
     of each sequence, as a pair of [seqs][tokens][heads][dim]; zeros where a sequence holds none.
     out: the pair to write instead of new tensors of `dtype`."""
+    if _elsewhere(cache, stream):
+        return _there(cache, stream, lambda: kv_read(cache, table, lens, tokens, starts, dtype, out))
     seqs = _kv_seqs(cache, table, lens, None)
     n = seqs.count
     if starts is not None:
-        _require(starts.dtype == torch.int32 and starts.shape == lens.shape
+        _require(starts.dtype is torch.int32 and starts.shape == (n,)
                  and starts.device == cache.device and starts.is_contiguous(), "starts")
     _require(0 <= tokens < 2**31 and (out is not None or dtype in _TYPES), "tokens or dtype")
-    with _On(cache.device, stream) as s:
-        if out is None:
-            shape = (n, tokens, cache.heads, cache.dim)
-            out = (torch.empty(shape, dtype=dtype, device=cache.device),
-                   torch.empty(shape, dtype=dtype, device=cache.device))
+    shape = (n, tokens, cache.heads, cache.dim)
+    if out is None:
+        k = cache.data.new_empty(shape, dtype=dtype)
+        v = torch.empty_like(k)
+    else:
         k, v = out
-        ck, cv = _kv_rows(cache, k, n, cache.heads, "k"), _kv_rows(cache, v, n, cache.heads, "v")
-        _require(k.shape[1] == tokens and v.shape[1] == tokens, "tokens of the output")
-        if tokens and n:
-            r = ctypes.byref
-            _check(lib().q4_kv_read(r(cache.c), r(seqs), None if starts is None else starts.data_ptr(),
-                                    tokens, r(ck), r(cv), s), "q4_kv_read")
+    ck, cv = _kv_rows(cache, k, shape, "k"), _kv_rows(cache, v, shape, "v")
+    if tokens and n:
+        r = ctypes.byref
+        status = lib().q4_kv_read(r(cache.c), r(seqs), None if starts is None else starts.data_ptr(),
+                                  tokens, r(ck), r(cv), torch._C._cuda_getCurrentRawStream(cache.index))
+        if status:
+            _check(status, "q4_kv_read")
     return k, v
 
 
@@ -445,36 +448,38 @@ def kv_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, lens: tor
     out: the result, of q's type if None; lse: binary32 [seqs][tokens][q_heads] to fill;
     ws: a workspace of kv_attention_workspace_bytes(dim), one for each stream, else a new
     one for this call."""
+    if _elsewhere(cache, stream):
+        return _there(cache, stream, lambda: kv_attention(cache, q, table, lens, new_lens, scale, window,
+                                                          softcap, alibi, out, lse, ws))
     seqs = _kv_seqs(cache, table, lens, new_lens)
-    n = seqs.count
-    _require(q.dim() == 4, "q")
-    tokens, heads = q.shape[1], q.shape[2]
-    cq = _kv_rows(cache, q, n, heads, "q")
-    scores = q4_kv_scores(cache.dim ** -0.5 if scale is None else scale, softcap, window)
+    shape = q.shape
+    _require(len(shape) == 4, "q")
+    n, tokens, heads = seqs.count, shape[1], shape[2]
+    cq = _kv_rows(cache, q, (n, tokens, heads, cache.dim), "q")
     _require(0 <= window < 2**31, "window")
+    scores = q4_kv_scores(cache.dim ** -0.5 if scale is None else scale, softcap, window, None)
     if alibi is not None:
-        _require(alibi.dtype == torch.float32 and alibi.shape == (heads,) and alibi.is_contiguous()
+        _require(alibi.dtype is torch.float32 and alibi.shape == (heads,) and alibi.is_contiguous()
                  and alibi.device == cache.device, "alibi")
         scores.alibi = alibi.data_ptr()
     if lse is not None:
-        _require(lse.dtype == torch.float32 and lse.shape == q.shape[:3] and lse.is_contiguous()
+        _require(lse.dtype is torch.float32 and lse.shape == (n, tokens, heads) and lse.is_contiguous()
                  and lse.device == cache.device, "lse")
-    with _On(cache.device, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
-        else:
-            _require(out.shape == q.shape, "out")
-        co = _kv_rows(cache, out, n, heads, "out")
-        if tokens == 0 or n == 0:
-            return out
-        if ws is None:
-            ws = workspace(kv_attention_workspace_bytes(cache.dim), cache.device)
-        else:
-            _require(ws.dtype == torch.uint8 and ws.device == cache.device and ws.is_contiguous(), "ws")
-        r = ctypes.byref
-        _check(lib().q4_kv_attention(r(cache.c), r(seqs), tokens, heads, r(cq), r(scores), r(co),
-                                     None if lse is None else lse.data_ptr(), ws.data_ptr(),
-                                     ws.numel(), s), "q4_kv_attention")
+        lse = lse.data_ptr()
+    if out is None:
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
+    co = _kv_rows(cache, out, shape, "out")
+    if tokens == 0 or n == 0:
+        return out
+    if ws is None:
+        ws = workspace(kv_attention_workspace_bytes(cache.dim), cache.device)
+    elif ws.dtype is not torch.uint8 or ws.device != cache.device or not ws.is_contiguous():
+        raise Q4Error(1, "ws")
+    r = ctypes.byref
+    status = lib().q4_kv_attention(r(cache.c), r(seqs), tokens, heads, r(cq), r(scores), r(co), lse,
+                                   ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(cache.index))
+    if status:
+        _check(status, "q4_kv_attention")
     return out
 
 

@@ -49,6 +49,8 @@ constexpr uint32_t kTimeoutFlag = 1u;
 constexpr int kRoom = 5;  // bits that scores may rise after ref was set before it moves again
 constexpr uint32_t kOnes = 0x3c003c00u;  // binary16 (1, 1)
 constexpr int kNoWindow = INT32_MAX - 64;  // positions are above -64
+constexpr int kJoin = 16;  // chunks of parts in a join; 16 parts each hold all CTAs
+constexpr float kNoRef = -1e30f;  // reference of a row that has seen nothing: finite, so that masked scores give weights of 0
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int DIM_, int NT_, bool SPLIT_, bool MOD_>
@@ -76,6 +78,7 @@ struct Cfg {
     static constexpr int OFF_BAR = OFF_ENT + WARPS * 2 * 32;
     static constexpr int OFF_PRE = OFF_BAR + WARPS * STAGES * 8;
     static constexpr int SMEM = OFF_PRE + (THREADS + 40) * 8;
+    static_assert(kJoin * RC * (DIM + 4) * 4 <= OFF_ENT, "the joins' sums");
     static_assert(PART * 4 <= RING, "a partial result fits the warp's ring");
     static_assert(SMEM <= 226 * 1024, "shared memory, with the static part");
 };
@@ -88,6 +91,7 @@ struct Entry {
     int32_t pad[2];
 };
 static_assert(sizeof(Entry) == 32, "entry");
+static_assert(16 * kJoin >= kMaxCtas, "chunks");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -204,7 +208,7 @@ __device__ __forceinline__ void write_lse(const AttnParams& P, int s, const RowA
 // A row without a position may hold any sums.
 __device__ __forceinline__ float result(float sum, float inv) { return inv == 0.0f ? 0.0f : sum * inv; }
 
-// exp2(a - b) for a <= b, 1 where both are the same infinity.
+// exp2(a - b) for a <= b, 1 where both are infinite.
 __device__ __forceinline__ float weight(float a, float b) { return a == b ? 1.0f : ex2(a - b); }
 
 // The warp's place in the work: unit u of sequence s, tile t of its span.
@@ -238,7 +242,7 @@ struct Warp {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) o[b][0][nt][v] = o[b][1][nt][v] = ob[nt][b][v] = 0.0f;
 #pragma unroll
-            for (int r = 0; r < F::RPL; ++r) ref[nt][r] = -INFINITY, l[nt][r] = 0.0f;
+            for (int r = 0; r < F::RPL; ++r) ref[nt][r] = kNoRef, l[nt][r] = 0.0f;
         }
         top_scale = F::SPLIT ? 0x0400u : 0x3c00u;
         lim = F::SPLIT ? 29.0f : 15.0f;
@@ -330,7 +334,7 @@ struct Warp {
                 const int mine = min(rt * F::RC + (nt * 4 + c) * F::RPL + r, rows - 1);
                 const RowAt ra = row_of(P, at.sp, h, group, mine);
                 pos[nt][r] = first + ra.i;
-                f[nt][r] = F::MOD ? kLog2e : fr * kLog2e;
+                f[nt][r] = F::MOD ? kLog2e : fmaxf(fr * kLog2e, 0x1p-140f);  // not 0: -inf is to stay that
                 if (F::MOD) scale[nt][r] = fr, slope[nt][r] = P.alibi ? P.alibi[ra.hq] : 0.0f;
             }
         }
@@ -360,7 +364,7 @@ struct Warp {
 #pragma unroll
             for (int r = 0; r < F::RPL; ++r) {
                 alpha[r] = ex2((float)(E - En));
-                ref[nt][r] += (float)(En - E);
+                if (ref[nt][r] != kNoRef) ref[nt][r] += (float)(En - E);
             }
             rescale(nt, alpha);
         }
@@ -403,10 +407,9 @@ struct Warp {
         return *reinterpret_cast<const uint32_t*>(&h);
     }
 
-    // Sixteen tokens (u: the first or the second of a record) from position p0 on. EDGE:
-    // some (row, token) is masked.
-    template <bool EDGE>
-    __device__ __forceinline__ void step(const AttnParams& P, const uint8_t* rec, int u, int p0, int lane) {
+    // Sixteen tokens (u: the first or the second of a record) from position p0 on; edge:
+    // some (row, token) is masked (the same for the whole warp).
+    __device__ __forceinline__ void step(const AttnParams& P, const uint8_t* rec, int u, int p0, bool edge, int lane) {
         constexpr int NB = F::NB, C = F::C, NT = F::NT, DIM = F::DIM;
         const int g = lane >> 2, c = lane & 3;
         // scores
@@ -460,7 +463,6 @@ struct Warp {
                     }
                 }
             }
-            const int window = P.window > 0 ? P.window : kNoWindow;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -472,9 +474,18 @@ struct Warp {
                         if (P.softcap > 0.0f) x = P.softcap * tanhf(x / P.softcap);
                         x = fmaf(slope[nt][r], (float)(key - pos[nt][r]), x);
                     }
-                    if (EDGE && (key > pos[nt][r] || key <= pos[nt][r] - window)) x = -INFINITY;
                     s[nt][v] = x;
                 }
+            if (edge) {
+                const int window = P.window > 0 ? P.window : kNoWindow;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int v = 0; v < F::VPT; ++v) {
+                        const int r = v % F::RPL, key = p0 + g + 8 * (v / F::RPL);
+                        if (key > pos[nt][r] || key <= pos[nt][r] - window) s[nt][v] = -INFINITY;
+                    }
+            }
         }
         float y[NT][F::VPT], top = -INFINITY;
 #pragma unroll
@@ -501,13 +512,11 @@ struct Warp {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    float p = ex2(y[nt][v]);
-                    if (EDGE && s[nt][v] == -INFINITY) p = 0.0f;
+                    const float p = ex2(y[nt][v]);
                     l[nt][0] += p;
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        float q = p * (b & 1 ? half_hi(dv[v][b / 2]) : half_lo(dv[v][b / 2]));
-                        if (EDGE && p == 0.0f) q = 0.0f;  // whatever the scale is
+                        const float q = p * (b & 1 ? half_hi(dv[v][b / 2]) : half_lo(dv[v][b / 2]));
                         const float hi = __uint_as_float(__float_as_uint(q) & 0xffffe000u);
                         pb[nt][b][v] = transposed(pack_half2(hi, q - hi));
                     }
@@ -523,18 +532,25 @@ struct Warp {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float p[2];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        p[r] = ex2(y[nt][2 * j + r]);
-                        if (EDGE && s[nt][2 * j + r] == -INFINITY) p[r] = 0.0f;
-                        l[nt][r] += p[r];
-                    }
-                    const uint32_t pt = transposed(pack_half2(p[0], p[1]));
-                    const uint32_t keep = EDGE ? nonzero_half2(pt) : kFull;
+                    const float p0_ = ex2(y[nt][2 * j]), p1_ = ex2(y[nt][2 * j + 1]);
+                    l[nt][0] += p0_, l[nt][F::RPL - 1] += p1_;
+                    const uint32_t pt = transposed(pack_half2(p0_, p1_));
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        pb[nt][b][j] = mul_half2(pt, __byte_perm(dv[j][0][b / 2], dv[j][1][b / 2], b & 1 ? 0x7632 : 0x5410)) & keep;
+                        pb[nt][b][j] = mul_half2(pt, __byte_perm(dv[j][0][b / 2], dv[j][1][b / 2], b & 1 ? 0x7632 : 0x5410));
+                }
+        }
+        // a masked token's weight is 0 whatever its scale is, NaN too
+        if (edge) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float a = s[nt][F::RPL * j] == -INFINITY ? 0.0f : 1.0f;
+                    const float z = s[nt][F::RPL * j + F::RPL - 1] == -INFINITY ? 0.0f : 1.0f;
+                    const uint32_t keep = nonzero_half2(transposed(pack_half2(a, z)));
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) pb[nt][b][j] &= keep;
                 }
         }
         // values
@@ -566,19 +582,19 @@ struct Warp {
     }
 
     // One record of 32 tokens from position p0 on.
-    template <bool EDGE>
     __device__ __forceinline__ void tile(const AttnParams& P, const uint8_t* rec, int p0, int lane) {
         const int window = P.window > 0 ? P.window : kNoWindow;
+        const bool edge = p0 + kGroup - 1 > minpos || p0 <= maxpos - window;
         uint32_t dv[F::NB / 2];
         load_words(rec + value_scale(F::DIM, lane, 0), dv);
         uint32_t m = abs_half2(dv[0]);
 #pragma unroll
         for (int i = 1; i < F::NB / 2; ++i) m = max_half2(m, abs_half2(dv[i]));
         m = max(m & 0xffffu, m >> 16);
-        if (EDGE && (p0 + lane > maxpos || p0 + lane <= minpos - window)) m = 0;
+        if (edge && (p0 + lane > maxpos || p0 + lane <= minpos - window)) m = 0;
         if (__any_sync(kFull, m > top_scale)) raise_scales(m);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) step<EDGE>(P, rec, u, p0 + 16 * u, lane);
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) step(P, rec, u, p0 + 16 * u, edge, lane);
     }
 
     // For each row of the lane, begin(row of the unit, ref, l) and pair(what that returned,
@@ -705,6 +721,25 @@ struct RowSum {
                 v[i][0] = fmaf(t.x, k, v[i][0]), v[i][1] = fmaf(t.y, k, v[i][1]);
             }
         }
+    }
+    __device__ __forceinline__ void load(const float* row, int lane) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float* const p = row + element(i, lane);
+            if constexpr (V == 4) {
+                const float4 t = __ldcg(reinterpret_cast<const float4*>(p));
+                v[i][0] = t.x, v[i][1] = t.y, v[i][2] = t.z, v[i][3] = t.w;
+            } else {
+                const float2 t = __ldcg(reinterpret_cast<const float2*>(p));
+                v[i][0] = t.x, v[i][1] = t.y;
+            }
+        }
+    }
+    __device__ __forceinline__ void add(const RowSum& o, float k) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i][j] = fmaf(o.v[i][j], k, v[i][j]);
     }
     __device__ __forceinline__ void keep(float* row, int lane) const {
 #pragma unroll
@@ -868,7 +903,6 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                 w.load_queries(P, at, rt_count, group, lane);
                 w.start();
             }
-            const int window = P.window > 0 ? P.window : kNoWindow;
             int p0 = (at.sp.tile0 + at.t) * kGroup;
             for (int i = 0; i < n; ++i) {
                 if (prod.filled >> stage & 1) {
@@ -879,11 +913,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                     if (dead) {
                         prod.left = 0;
                     } else {
-                        const uint8_t* rec = ring + stage * F::REC;
-                        if (p0 + kGroup - 1 <= w.minpos && p0 > w.maxpos - window)
-                            w.template tile<false>(P, rec, p0, lane);
-                        else
-                            w.template tile<true>(P, rec, p0, lane);
+                        w.tile(P, ring + stage * F::REC, p0, lane);
                     }
                 }
                 __syncwarp();
@@ -962,7 +992,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
             for (int row = 0; row < n; ++row) {
                 if (task++ % F::WARPS != warp) continue;
                 const bool in = run_mask >> lane & 1;
-                const float m = in ? ml[lane * 2 * F::RC + row] : -INFINITY;
+                const float m = in ? ml[lane * 2 * F::RC + row] : kNoRef;
                 const float top = warp_max(m);
                 const float k = in ? weight(m, top) : 0.0f;
                 const float l = warp_sum(in ? k * ml[lane * 2 * F::RC + F::RC + row] : 0.0f);
@@ -1011,24 +1041,44 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
         const int h = rt_count == 1 ? en.u : en.u / rt_count, row0 = (en.u - h * rt_count) * F::RC;
         const Span sp = span_at(P, en.s);
         auto part = [&](int cta) { return P.parts + ((int64_t)cta * 2 + (cta == i0 ? slot0 : 0)) * F::WPART; };
-        for (int row = warp; row < min(F::RC, rows - row0); row += F::WARPS) {
-            float top = -INFINITY, l = 0.0f;
-            for (int c0 = i0; c0 <= i1; c0 += 32)
-                if (c0 + lane <= i1) top = fmaxf(top, __ldcg(part(c0 + lane) + F::RC * F::DIM + row));
-            top = warp_max(top);
+        // chunks of parts by warp, all loads of one in flight at once; the chunks' sums meet in
+        // the rings' memory
+        const int n = i1 - i0 + 1, nrows = min(F::RC, rows - row0);
+        const int chunks = n <= 8 * kJoin ? (n + 7) / 8 : (n + 15) / 16;
+        const int per = n <= 8 * kJoin ? 8 : 16;
+        float* const sums = reinterpret_cast<float*>(smem);  // [row][chunk][ref, l][DIM]: no more than kJoin chunks
+        __syncthreads();
+        for (int task = warp; task < nrows * chunks; task += F::WARPS) {
+            const int row = task / chunks, c0 = (task - row * chunks) * per, m = min(per, n - c0);
             RowSum<F::DIM> sum;
-            for (int c0 = i0; c0 <= i1; c0 += 32) {
-                float k = 0.0f;
-                if (c0 + lane <= i1) {
-                    const float* const p = part(c0 + lane) + F::RC * F::DIM + row;
-                    k = weight(__ldcg(p), top);
-                    l = fmaf(k, __ldcg(p + F::RC), l);
-                }
-                const int n = min(32, i1 + 1 - c0);
-#pragma unroll 8
-                for (int i = 0; i < n; ++i) sum.template add<true>(part(c0 + i) + row * F::DIM, __shfl_sync(kFull, k, i), lane);
+            float ref = kNoRef, l = 0.0f;
+            if (lane < m) {
+                const float* const q = part(i0 + c0 + lane) + F::RC * F::DIM + row;
+                ref = __ldcg(q), l = __ldcg(q + F::RC);
             }
-            sum.write(P, en.s, row_of(P, sp, h, group, row0 + row), top, warp_sum(l), lane);
+            RowSum<F::DIM> v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < m) v[i].load(part(i0 + c0 + i) + row * F::DIM, lane);
+            const float top = warp_max(ref);
+            const float k = lane < m ? weight(ref, top) : 0.0f;
+            l = warp_sum(l * k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum.add(v[i], __shfl_sync(kFull, k, i));
+            for (int i = 8; i < m; ++i) sum.template add<true>(part(i0 + c0 + i) + row * F::DIM, __shfl_sync(kFull, k, i), lane);
+            float* const to = sums + task * (F::DIM + 4);
+            sum.keep(to, lane);
+            if (lane == 0) to[F::DIM] = top, to[F::DIM + 1] = l;
+        }
+        __syncthreads();
+        for (int row = warp; row < nrows; row += F::WARPS) {
+            const float* const from = sums + row * chunks * (F::DIM + 4);
+            const float ref = lane < chunks ? from[lane * (F::DIM + 4) + F::DIM] : kNoRef;
+            const float top = warp_max(ref), k = lane < chunks ? weight(ref, top) : 0.0f;
+            const float l = warp_sum(lane < chunks ? k * from[lane * (F::DIM + 4) + F::DIM + 1] : 0.0f);
+            RowSum<F::DIM> sum;
+            for (int i = 0; i < chunks; ++i) sum.template add<false>(from + i * (F::DIM + 4), __shfl_sync(kFull, k, i), lane);
+            sum.write(P, en.s, row_of(P, sp, h, group, row0 + row), top, l, lane);
         }
     }
 }
