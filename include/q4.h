@@ -306,8 +306,8 @@ typedef struct {
  *   k, v : [seqs->count][tokens][cache->heads][cache->dim]
  * tokens >= 0; no work is enqueued for zero tokens or sequences.
  * Errors: Q4_ERR_INVALID_ARG, Q4_ERR_MISALIGNED, Q4_ERR_UNSUPPORTED (dim, type, device),
- * Q4_ERR_CUDA. Q4_ERR_INVALID_ARG too for count * tokens * heads (twice that for dim 256) at
- * or above 2^31. */
+ * Q4_ERR_CUDA. Q4_ERR_INVALID_ARG too for count * heads * ((tokens + 6) / 8 + 1) at or
+ * above 2^31. */
 q4_status q4_kv_write(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, const q4_rows* k,
                       const q4_rows* v, void* stream);
 

@@ -76,9 +76,8 @@ q4_status move_call(bool write, const q4_kv_cache* cache, const q4_kv_seqs* seqs
     if ((s = check_rows(v, seqs->count, tokens, cache->heads, cache->dim, !write)) != Q4_OK) return s;
     if (!aligned(starts, 4)) return Q4_ERR_MISALIGNED;
     if (seqs->count == 0 || tokens == 0) return Q4_OK;
-    const int chunks = cache->dim / 32 / q4kv::chunk_blocks(cache->dim);
-    const int64_t per_token = (int64_t)cache->heads * chunks;
-    if ((int64_t)seqs->count * tokens > INT32_MAX / per_token) return Q4_ERR_INVALID_ARG;
+    const int64_t runs = ((int64_t)tokens + q4kv::kRun - 2) / q4kv::kRun + 1;
+    if (seqs->count * runs > INT32_MAX / cache->heads) return Q4_ERR_INVALID_ARG;
     int num_sms = 0;
     if ((s = ensure_device(&num_sms)) != Q4_OK) return s;
     q4kv::MoveParams P = {};
@@ -88,7 +87,8 @@ q4_status move_call(bool write, const q4_kv_cache* cache, const q4_kv_seqs* seqs
     P.v = rows_of(v);
     P.starts = starts;
     P.tokens = tokens;
-    P.items = (int32_t)((int64_t)seqs->count * tokens * per_token);
+    P.runs = (int32_t)runs;
+    P.items = (int32_t)(seqs->count * runs * cache->heads);
     if (cuda_failed(q4kv::launch_kv_move(write, cache->dim, P, static_cast<cudaStream_t>(stream)))) return Q4_ERR_CUDA;
     count_launches(1);
     return Q4_OK;

@@ -23,6 +23,7 @@
 namespace q4kv {
 
 constexpr int kGroup = 32;           // tokens of a record
+constexpr int kRun = 8;              // tokens that a warp writes or reads back
 constexpr uint32_t kBadPage = 0x100; // workspace flag: a page index outside the cache
 
 __host__ __device__ constexpr int record_bytes(int dim) { return 36 * dim; }
@@ -84,7 +85,8 @@ struct MoveParams {  // write and read
     Rows k, v;
     const int32_t* starts;  // read: first position of each sequence, nullptr: 0
     int32_t tokens;
-    int32_t items;  // seqs * tokens * heads * chunks
+    int32_t runs;   // of kRun positions that `tokens` positions touch at most
+    int32_t items;  // seqs * runs * heads
 };
 
 struct AttnParams {
