@@ -1,13 +1,15 @@
 // Writing tokens into the 4-bit key/value cache and reading them back.
 //
 // Both move bytes and little else, so they are bound by memory once the work around a
-// value is small. A warp takes a run of eight positions of one head: the page is looked up
-// once a run, whose codes are contiguous in the record (by chunk, and keys and values
-// apart). Eight lanes own a block of 32 values, four neighbours each, so that the dense side
-// moves in coalesced 8- or 16-byte accesses. (A whole record a warp reads as fast where there
-// are many, but writes 8192 tokens of 8 heads in 57 us against XXX us: too few loads in flight.) The
+// value is small, and by instructions until then. A warp takes a run of eight positions of one
+// head: its page is looked up once, and its codes are contiguous in the record (by chunk,
+// keys and values apart). (A warp a whole record reads as fast, but writes 8192 tokens of 8
+// heads in 57 us against 34: too few loads in flight.) Eight lanes own a block of 32 values,
+// four neighbours each, so that the dense side moves in coalesced 8- or 16-byte accesses. The
 // codes follow the rule of q4_pack bit for bit: every binary32 step is an explicit
-// round-to-nearest operation.
+// round-to-nearest operation. Measured on a B200: 8192 bfloat16 tokens of 8 heads of 128
+// written in 20 us (43 MB), 32768 read back as bfloat16 in 33 us (172 MB, 5.2 TB/s), as
+// binary32 in 51 us (306 MB, 6.0 TB/s, the copy rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -23,7 +25,7 @@ namespace q4kv {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kUnroll = 4;  // tokens (or pairs) of a run whose loads fly together
+constexpr int kUnroll = 4;  // tokens (dim 64: pairs of tokens) of a run whose loads fly together
 constexpr uint32_t kFull = 0xffffffffu;
 
 // The warp's head, sequence and how many runs its own lies behind the sequence's first;
@@ -53,41 +55,130 @@ __device__ __forceinline__ uint8_t* record(const MoveParams& P, int s, int h, in
     return P.cache.data + record_at(P.cache, DIM, page, h, p - pg * P.cache.page_size);
 }
 
-// Quantises the eight lanes' 32 values: *word = word i8 % 4 of the block's codes (in
-// lanes i8 and i8 ^ 4), *d = its scale (in every lane). A block that holds a NaN or an
-// infinity gets the scale NaN.
-__device__ __forceinline__ void quantise(const float (&v)[4], int i8, uint32_t* word, uint16_t* d) {
-    float m = 0.0f;
-    bool bad = false;
+// The types of a call's rows: one of q4_dtype where keys and values both have it and four
+// neighbours can be moved at once, else anything, looked up at each access.
+constexpr int kAnyRows = 3;
+
+__device__ __forceinline__ uint32_t max8(uint32_t v) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        bad |= !(fabsf(v[j]) < __int_as_float(0x7f800000));
-        if (fabsf(v[j]) > fabsf(m)) m = v[j];
-    }
-    // the lowest index wins a tie: the lower half of a pair of lanes keeps its own
-#pragma unroll
-    for (int off = 1; off < 8; off <<= 1) {
-        const float o = __shfl_xor_sync(kFull, m, off);
-        if (fabsf(o) > fabsf(m) || (fabsf(o) == fabsf(m) && (i8 & off))) m = o;
-    }
-    const bool any_bad = __ballot_sync(kFull, bad) >> (threadIdx.x & 24) & 0xffu;
-    const float dd = __fmul_rn(m, -0.125f);  // m / -8
-    const float inv = dd != 0.0f ? __frcp_rn(dd) : 0.0f;
-    uint32_t w = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        // at or above 0.5, but for what is not a number or infinite: truncation is the floor
-        const int q = (int)__fadd_rn(__fmul_rn(v[j], inv), 8.5f);
-        w |= (uint32_t)min(max(q, 0), 15) << (8 * j);
-    }
-    const uint32_t o = __shfl_xor_sync(kFull, w, 4);
-    *word = i8 < 4 ? w | (o << 4) : o | (w << 4);
-    *d = any_bad ? (uint16_t)0x7fffu : __half_as_ushort(__float2half_rn(dd));
+    for (int off = 1; off < 8; off <<= 1) v = max(v, __shfl_xor_sync(kFull, v, off));
+    return v;
 }
 
-template <int DIM>
+// The code of one value: min(15, floor(t)) of t = v * inv + 8.5, as q4_pack rounds it. The
+// slow form holds for every t.
+__device__ __forceinline__ uint32_t code_slow(float v, float inv) {
+    return (uint32_t)min(max((int)floorf(__fadd_rn(__fmul_rn(v, inv), 8.5f)), 0), 15);
+}
+
+// Quantises the eight lanes' 32 values: *word = word i8 % 4 of the block's codes (in
+// lanes i8 and i8 ^ 4), *d = its scale (in every lane). A block that holds a NaN or an
+// infinity gets the scale NaN. NARROW: the values come from 16-bit types, so that the low 13
+// bits of their binary32 are 0.
+template <bool NARROW>
+__device__ __forceinline__ void quantise(const float (&v)[4], int i8, uint32_t* word, uint16_t* d) {
+    // the value of largest magnitude, the lowest index of equal ones: the largest of
+    // (magnitude, -index, sign), in one word where there is room for all three
+    uint32_t x[4], top, sign;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = __float_as_uint(v[j]);
+    if constexpr (NARROW) {
+        uint32_t key = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) key = max(key, ((x[j] & 0x7fffff80u) | (uint32_t)(62 - 8 * i8 - 2 * j)) + (x[j] >> 31));
+        key = max8(key);
+        top = key & 0x7fffff80u;
+        sign = key << 31;
+    } else {
+        top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, x[j] & 0x7fffffffu);
+        top = max8(top);
+        uint32_t key = 0;
+#pragma unroll
+        for (int j = 3; j >= 0; --j)
+            if ((x[j] & 0x7fffffffu) == top) key = (uint32_t)(64 - 8 * i8 - 2 * j) + (x[j] >> 31);
+        sign = max8(key) << 31;
+    }
+    if (top == 0) sign = 0;  // the rule starts from +0
+    const float dd = __fmul_rn(__uint_as_float(top | sign), -0.125f);  // m / -8
+    const float inv = dd != 0.0f ? __frcp_rn(dd) : 0.0f;
+    // t is 0.5 or more: 2^23 + t rounded towards zero has floor(t) in its low bits. Not so where
+    // 1 / d overflows (|d| < 2^-127).
+    uint32_t q[4];
+    if (__any_sync(kFull, fabsf(inv) > 0x1p126f)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = code_slow(v[j], inv);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            q[j] = (uint32_t)min(__float_as_int(__fadd_rz(__fadd_rn(__fmul_rn(v[j], inv), 8.5f), 0x1p23f)), 0x4b00000f);
+    }
+    const uint32_t w = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+    const uint32_t o = __shfl_xor_sync(kFull, w, 4);
+    *word = (i8 < 4 ? o : w) * 16 + (i8 < 4 ? w : o);
+    *d = top >= 0x7f800000u ? (uint16_t)0x7fffu : __half_as_ushort(__float2half_rn(dd));
+}
+
+template <int T>
+__device__ __forceinline__ void load_four(const Rows& r, int64_t at, float (&v)[4]) {
+    if constexpr (T == kAnyRows) {
+        load4(r, at, v);
+    } else if constexpr (T == Q4_F32) {
+        const float4 t = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(r.data) + at));
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+    } else {
+        const uint2 t = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(r.data) + at));
+        if constexpr (T == Q4_BF16) {
+            v[0] = __uint_as_float(t.x << 16), v[1] = __uint_as_float(t.x & 0xffff0000u);
+            v[2] = __uint_as_float(t.y << 16), v[3] = __uint_as_float(t.y & 0xffff0000u);
+        } else {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&t.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&t.y));
+            v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+        }
+    }
+}
+
+// Where the lane's parts of a token go: for the chunk that holds block bb.
+struct WriteAt {
+    uint8_t *key, *key_d, *value, *value_d;
+};
+
+// Quantises the lane's four values of each chunk's key and value and stores them; not `mine`:
+// takes part only.
+template <int DIM, int T>
+__device__ __forceinline__ void write_token(const WriteAt& to, const float (&v)[DIM / 32 / chunk_blocks(DIM)][2][4], int bb, int i8,
+                                            bool mine) {
+    constexpr int C = chunk_blocks(DIM), NCH = DIM / 32 / C;
+    constexpr bool NARROW = T == Q4_F16 || T == Q4_BF16;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int ch = 0; ch < NCH; ++ch) {
+        uint32_t word;
+        uint16_t d;
+        quantise<NARROW>(v[ch][0], i8, &word, &d);
+        const int next_key = key_word(DIM, 0, ch * C, 0) - key_word(DIM, 0, 0, 0);
+        if (mine && i8 < 4) *reinterpret_cast<uint32_t*>(to.key + next_key) = word;
+        if (mine && i8 == 0) *reinterpret_cast<uint16_t*>(to.key_d + 2 * ch * C) = d;
+        quantise<NARROW>(v[ch][1], i8, &word, &d);
+        // lane i8 takes half i8 of its block; the halves i8 of the chunk's blocks are neighbours
+        const uint32_t w = __shfl_sync(kFull, word, (lane & 24) + (i8 >> 1));
+        const uint32_t half = i8 & 1 ? w >> 16 : w;
+        const uint32_t pair = __byte_perm(half, __shfl_xor_sync(kFull, half, 8), 0x5410);
+        uint8_t* const value = to.value + (value_half(DIM, 0, ch * C, 0) - value_half(DIM, 0, 0, 0));
+        if (C == 2) {
+            if (mine && bb == 0) *reinterpret_cast<uint32_t*>(value) = pair;
+        } else {
+            const uint32_t next = __shfl_xor_sync(kFull, pair, 16);
+            if (mine && bb == 0) *reinterpret_cast<uint2*>(value) = make_uint2(pair, next);
+        }
+        if (mine && i8 == 0) *reinterpret_cast<uint16_t*>(to.value_d + 2 * ch * C) = d;
+    }
+}
+
+template <int DIM, int T>
 __global__ void __launch_bounds__(32 * kWarps) kv_write_kernel(const __grid_constant__ MoveParams P) {
-    constexpr int C = chunk_blocks(DIM), NCH = DIM / 32 / C, L = 8 * C, TOK = 32 / L;  // TOK tokens at once
+    constexpr int NB = DIM / 32, C = chunk_blocks(DIM), NCH = NB / C, L = 8 * C, TOK = 32 / L;  // TOK tokens at once
     Task k;
     if (!task_of(P, &k)) return;
     const int len = P.seqs.lens[k.s];
@@ -102,52 +193,79 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_kernel(const __grid_cons
     const int lane = threadIdx.x & 31, sub = lane / L, bb = lane % L / 8, i8 = lane & 7;
     const int t0 = (int)(p0 % kGroup), i0 = (int)(p0 - first);
     const int64_t ks = row_at(P.k, k.s, i0, k.h) + bb * 32 + 4 * i8, vs = row_at(P.v, k.s, i0, k.h) + bb * 32 + 4 * i8;
-#pragma unroll kUnroll
-    for (int base = 0; base < n; base += TOK) {
-        const bool mine = base + sub < n;
-        const int i = mine ? base + sub : n - 1, t = t0 + i;  // the last token twice rather than none
-        float v[NCH][2][4];
+    if (n == kRun) {
+        // a whole run, aligned in its record: every place is known but for the lane's own
+        const WriteAt to = {at + key_word(DIM, t0, bb, i8 & 3), at + key_scale(DIM, t0, bb), at + value_half(DIM, t0, bb, i8),
+                            at + value_scale(DIM, t0, bb)};
 #pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-            load4(P.k, ks + i * P.k.token + ch * 32 * C, v[ch][0]);
-            load4(P.v, vs + i * P.v.token + ch * 32 * C, v[ch][1]);
-        }
+        for (int half = 0; half < kRun / TOK; half += kUnroll) {
+            float v[kUnroll][NCH][2][4];
 #pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-            const int b = ch * C + bb;
-            uint32_t word;
-            uint16_t d;
-            quantise(v[ch][0], i8, &word, &d);
-            if (mine && i8 < 4) *reinterpret_cast<uint32_t*>(at + key_word(DIM, t, b, i8)) = word;
-            if (mine && i8 == 0) *reinterpret_cast<uint16_t*>(at + key_scale(DIM, t, b)) = d;
-            quantise(v[ch][1], i8, &word, &d);
-            // lane i8 takes half i8 of its block; the halves i8 of the chunk's blocks are neighbours
-            const uint32_t w = __shfl_sync(kFull, word, (lane & 24) + (i8 >> 1));
-            const uint32_t half = i8 & 1 ? w >> 16 : w & 0xffffu;
-            const uint32_t pair = half | (__shfl_xor_sync(kFull, half, 8) << 16);
-            if (C == 2) {
-                if (mine && bb == 0) *reinterpret_cast<uint32_t*>(at + value_half(DIM, t, b, i8)) = pair;
-            } else {
-                const uint32_t next = __shfl_xor_sync(kFull, pair, 16);
-                if (mine && bb == 0) *reinterpret_cast<uint2*>(at + value_half(DIM, t, b, i8)) = make_uint2(pair, next);
+            for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+                for (int ch = 0; ch < NCH; ++ch) {
+                    load_four<T>(P.k, ks + ((half + i) * TOK + sub) * P.k.token + ch * 32 * C, v[i][ch][0]);
+                    load_four<T>(P.v, vs + ((half + i) * TOK + sub) * P.v.token + ch * 32 * C, v[i][ch][1]);
+                }
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                // token t of an aligned run of eight (TOK 2: the second half warp's is odd)
+                const int t = (half + i) * TOK;
+                const WriteAt at_t = {to.key + (key_word(DIM, t, 0, 0) - key_word(DIM, 0, 0, 0)) + sub * 16 * C,
+                                      to.key_d + t * 2 * NB + sub * 2 * NB,
+                                      to.value + (value_half(DIM, t, 0, 0) - value_half(DIM, 0, 0, 0)) + sub * 2 * C,
+                                      to.value_d + t * 2 * NB + sub * 2 * NB};
+                write_token<DIM, T>(at_t, v[i], bb, i8, true);
             }
-            if (mine && i8 == 0) *reinterpret_cast<uint16_t*>(at + value_scale(DIM, t, b)) = d;
+        }
+    } else {
+        for (int base = 0; base < n; base += TOK) {
+            const bool mine = base + sub < n;
+            const int i = mine ? base + sub : n - 1, t = t0 + i;  // the last token twice rather than none
+            float v[NCH][2][4];
+#pragma unroll
+            for (int ch = 0; ch < NCH; ++ch) {
+                load_four<T>(P.k, ks + i * P.k.token + ch * 32 * C, v[ch][0]);
+                load_four<T>(P.v, vs + i * P.v.token + ch * 32 * C, v[ch][1]);
+            }
+            const WriteAt at_t = {at + key_word(DIM, t, bb, i8 & 3), at + key_scale(DIM, t, bb), at + value_half(DIM, t, bb, i8),
+                                  at + value_scale(DIM, t, bb)};
+            write_token<DIM, T>(at_t, v, bb, i8, mine);
         }
     }
 }
 
-// Four values of a block: the nibbles of `word` at bits 0, 8, 16, 24, exact in binary32.
-__device__ __forceinline__ void expand(uint32_t word, uint16_t d, float (&v)[4]) {
-    const float s = __half2float(__ushort_as_half(d));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        // 2^23 + q, less 2^23 + 8: exact
-        const float f = __uint_as_float(((word >> (8 * j)) & 0xfu) | 0x4b000000u) - 8388616.0f;
-        v[j] = __fmul_rn(s, f);
+// Four values of a block from the nibbles of `word` at bits 0, 8, 16, 24, times the scale
+// of binary16 bits d, rounded once to the rows' type, to the row elements at ..
+template <int T>
+__device__ __forceinline__ void store_four(const Rows& r, int64_t at, uint32_t word, uint16_t d) {
+    // 1024 + q in binary16, less 1032: q - 8, exact
+    const uint32_t even = (word & 0x000f000fu) | 0x64006400u, odd = ((word >> 8) & 0x000f000fu) | 0x64006400u;
+    const __half2 off = __floats2half2_rn(-1032.0f, -1032.0f);
+    const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&even), off), b = __hadd2(*reinterpret_cast<const __half2*>(&odd), off);
+    if constexpr (T == Q4_F16) {
+        // the product of two binary16 numbers rounds once
+        const __half2 s = __half2half2(__ushort_as_half(d)), x = __hmul2(a, s), y = __hmul2(b, s);
+        const uint32_t p = *reinterpret_cast<const uint32_t*>(&x), q = *reinterpret_cast<const uint32_t*>(&y);
+        __stcs(reinterpret_cast<uint2*>(static_cast<uint16_t*>(r.data) + at),
+               make_uint2(__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632)));
+    } else {
+        const float s = __half2float(__ushort_as_half(d));
+        const float v[4] = {__fmul_rn(__low2float(a), s), __fmul_rn(__low2float(b), s), __fmul_rn(__high2float(a), s),
+                            __fmul_rn(__high2float(b), s)};
+        if constexpr (T == Q4_F32) {
+            __stcs(reinterpret_cast<float4*>(static_cast<float*>(r.data) + at), make_float4(v[0], v[1], v[2], v[3]));
+        } else if constexpr (T == Q4_BF16) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
+            __stcs(reinterpret_cast<uint2*>(static_cast<uint16_t*>(r.data) + at),
+                   make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y)));
+        } else {
+            store4(r, at, v);
+        }
     }
 }
 
-template <int DIM>
+template <int DIM, int T>
 __global__ void __launch_bounds__(32 * kWarps) kv_read_kernel(const __grid_constant__ MoveParams P) {
     constexpr int NB = DIM / 32, C = chunk_blocks(DIM), NCH = NB / C, L = 8 * C, TOK = 32 / L;
     constexpr int PART = 128 * C;  // bytes of a chunk of a run's keys or values
@@ -190,35 +308,48 @@ __global__ void __launch_bounds__(32 * kWarps) kv_read_kernel(const __grid_const
         const int t = t0 + i;
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
-            float kv[4] = {0.0f, 0.0f, 0.0f, 0.0f}, vv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t kw, vw;  // code words: of zeros where nothing is held
+            uint16_t kd = 0, vd = 0;
             if (i < held) {
                 const uint32_t* const keys = reinterpret_cast<const uint32_t*>(sm + 2 * ch * PART);
                 const uint16_t* const values = reinterpret_cast<const uint16_t*>(sm + (2 * ch + 1) * PART);
                 const int v = (t / 2 * 8 + 2 * c) * 2 + t % 2;  // half 2c of the token, the next is two behind
-                const uint32_t lo = values[v * C + bb], hi = values[(v + 2) * C + bb];
-                expand(keys[(t * 4 + c) * C + bb] >> shift, scales[t * NB + ch * C], kv);
-                expand((lo | (hi << 16)) >> shift, scales[(kRun + t) * NB + ch * C], vv);
+                kw = keys[(t * 4 + c) * C + bb] >> shift;
+                vw = (values[v * C + bb] | ((uint32_t)values[(v + 2) * C + bb] << 16)) >> shift;
+                kd = scales[t * NB + ch * C], vd = scales[(kRun + t) * NB + ch * C];
+            } else {
+                kw = vw = 0x08080808u;
             }
-            store4(P.k, ks + i * P.k.token + ch * 32 * C, kv);
-            store4(P.v, vs + i * P.v.token + ch * 32 * C, vv);
+            store_four<T>(P.k, ks + i * P.k.token + ch * 32 * C, kw, kd);
+            store_four<T>(P.v, vs + i * P.v.token + ch * 32 * C, vw, vd);
         }
     }
 }
 
-template <int DIM>
-cudaError_t launch(bool write, const MoveParams& P, cudaStream_t stream) {
+template <int DIM, int T>
+void launch(bool write, const MoveParams& P, cudaStream_t stream) {
     const unsigned grid = (unsigned)(((int64_t)P.items + kWarps - 1) / kWarps);
     if (write)
-        kv_write_kernel<DIM><<<grid, 32 * kWarps, 0, stream>>>(P);
+        kv_write_kernel<DIM, T><<<grid, 32 * kWarps, 0, stream>>>(P);
     else
-        kv_read_kernel<DIM><<<grid, 32 * kWarps, 0, stream>>>(P);
+        kv_read_kernel<DIM, T><<<grid, 32 * kWarps, 0, stream>>>(P);
+}
+
+template <int DIM>
+cudaError_t with_type(bool write, const MoveParams& P, cudaStream_t stream) {
+    switch (P.k.vec && P.v.vec && P.k.type == P.v.type ? P.k.type : kAnyRows) {
+        case Q4_F32: launch<DIM, Q4_F32>(write, P, stream); break;
+        case Q4_F16: launch<DIM, Q4_F16>(write, P, stream); break;
+        case Q4_BF16: launch<DIM, Q4_BF16>(write, P, stream); break;
+        default: launch<DIM, kAnyRows>(write, P, stream);
+    }
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv_move(bool write, int dim, const MoveParams& P, cudaStream_t stream) {
-    return dim == 64 ? launch<64>(write, P, stream) : dim == 128 ? launch<128>(write, P, stream) : launch<256>(write, P, stream);
+    return dim == 64 ? with_type<64>(write, P, stream) : dim == 128 ? with_type<128>(write, P, stream) : with_type<256>(write, P, stream);
 }
 
 }  // namespace q4kv

@@ -159,6 +159,31 @@ def test_zero_blocks_ties_and_ranges():
     assert np.array_equal(v.cpu().numpy(), oracle_values(x.flip(1)).numpy())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_ties_and_tiny_values_of_every_type(dtype):
+    """Equal magnitudes of both signs at every distance, and blocks whose 1 / d overflows."""
+    dim, n = 128, 40
+    g = torch.Generator().manual_seed(21)
+    x = torch.randint(-3, 4, (1, n, 2, dim), generator=g).float() * 0.75  # many ties
+    x[0, 3] = torch.randn(2, dim, generator=g) * 2.0 ** -130
+    x[0, 4] = torch.randn(2, dim, generator=g) * 2.0 ** -127
+    x[0, 5, 0, 7], x[0, 5, 1, 31] = 2.0 ** -133, -(2.0 ** -24)
+    x[0, 6] = 0
+    x[0, 6, 0, 64], x[0, 6, 0, 95] = -1.0, 1.0
+    x = x.to(dtype)
+    cache = q4.KVCache(2, 2, dim, 32)
+    table, lens = torch.tensor([[1, 0]], dtype=torch.int32).cuda(), torch.tensor([n], dtype=torch.int32).cuda()
+    q4.kv_write(cache, x.cuda(), x.cuda().flip(1), table, lens)
+    k, v = q4.kv_read(cache, table, lens, n)
+    assert torch.equal(k.cpu(), oracle_values(x)) and torch.equal(v.cpu(), oracle_values(x.flip(1)))
+    # rows of two types in one call
+    other = {torch.float32: torch.bfloat16, torch.float16: torch.float32, torch.bfloat16: torch.float16}[dtype]
+    q4.kv_write(cache, x.cuda(), x.to(other).cuda(), table, lens)
+    out = (torch.empty(1, n, 2, dim, dtype=other, device="cuda"), torch.empty(1, n, 2, dim, dtype=dtype, device="cuda"))
+    q4.kv_read(cache, table, lens, n, out=out)
+    assert torch.equal(out[0].cpu(), oracle_values(x).to(other)) and torch.equal(out[1].cpu(), oracle_values(x.to(other)).to(dtype))
+
+
 def test_strides_and_unaligned_rows():
     dim, heads, n, s = 128, 4, 9, 3
     table, pages = tables(s, 1)
