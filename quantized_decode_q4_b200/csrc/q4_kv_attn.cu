@@ -65,7 +65,8 @@ struct Cfg {
     // warps an SM: as many as hold the row tile's operands and sums in registers without
     // spilling (spills go through what little L1 the rings leave)
     static constexpr int WARPS = DIM == 64 ? (NT == 1 ? 16 : 12) : DIM == 128 && NT == 1 ? 12 : 8;
-    static constexpr int STAGES = DIM == 64 ? 4 : DIM == 128 ? (NT == 1 ? 3 : 4) : 2;
+    static constexpr int STAGES = DIM == 64 ? 4 : DIM == 128 ? (NT == 1 ? 2 : 4) : 2;
+    static_assert((STAGES & (STAGES - 1)) == 0, "a power of two");
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int ROW = DIM + 8;             // floats of a row of a partial result in shared memory
     static constexpr int PART = RC * ROW;
@@ -77,7 +78,8 @@ struct Cfg {
     static constexpr int OFF_ENT = OFF_ML + WARPS * 2 * 2 * RC * 4;
     static constexpr int OFF_BAR = OFF_ENT + WARPS * 2 * 32;
     static constexpr int OFF_PRE = OFF_BAR + WARPS * STAGES * 8;
-    static constexpr int SMEM = OFF_PRE + (THREADS + 40) * 8;
+    static constexpr int OFF_HELD = OFF_PRE + (THREADS + 40) * 8;
+    static constexpr int SMEM = OFF_HELD + WARPS * 112;
     static_assert(kJoin * RC * (DIM + 4) * 4 <= OFF_ENT, "the joins' sums");
     static_assert(PART * 4 <= RING, "a partial result fits the warp's ring");
     static_assert(SMEM <= 226 * 1024, "shared memory, with the static part");
@@ -107,10 +109,10 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 }
 
 // The same with depth 8.
-__device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(b0));
+__device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0, float c0, float c1, float c2, float c3) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%8,%9,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(b0), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 __device__ __forceinline__ uint32_t transposed(uint32_t a) {
@@ -129,17 +131,24 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint32_t abs_half2(uint32_t a) { return a & 0x7fff7fffu; }
-
 // The larger of each half, a NaN yielding to a number.
 __device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
     const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// All bits of the halves of `a` that are not zero.
-__device__ __forceinline__ uint32_t nonzero_half2(uint32_t a) {
-    return __hne2_mask(*reinterpret_cast<const __half2*>(&a), __floats2half2_rn(0.0f, 0.0f));
+// Whether both halves are at most those of `top`.
+__device__ __forceinline__ bool within_half2(uint32_t a, uint32_t top) {
+    return __hble2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&top));
+}
+
+__device__ __forceinline__ uint32_t both_low(uint32_t a) {
+    const __half2 h = __low2half2(*reinterpret_cast<const __half2*>(&a));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t both_high(uint32_t a) {
+    const __half2 h = __high2half2(*reinterpret_cast<const __half2*>(&a));
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <int N>
@@ -217,6 +226,30 @@ struct Place {
     Span sp;
 };
 
+// What a warp looks at where a page, a unit or a sequence ends is held in shared memory: its
+// loop needs the registers. Every lane writes and reads the same values.
+struct Held {
+    int64_t start;             // first tile of the unit that the warp works on
+    Place at;                  // and its place
+    Place next;                // of the next record to be copied
+    int page, base;            // ordinal of its page in the sequence's table; lane i of the producer holds entry base + i
+    int unit_left;             // records of its unit behind that page
+    int minpos, maxpos;        // over the unit's rows that have a position
+    int pad;
+};
+static_assert(sizeof(Held) <= 112, "held");
+
+__device__ __forceinline__ Place get(const volatile Place& v) {
+    Place p;
+    p.s = v.s, p.u = v.u, p.t = v.t;
+    p.sp.tile0 = v.sp.tile0, p.sp.n = v.sp.n, p.sp.len = v.sp.len, p.sp.nl = v.sp.nl;
+    return p;
+}
+__device__ __forceinline__ void put(volatile Place& v, const Place& p) {
+    v.s = p.s, v.u = p.u, v.t = p.t;
+    v.sp.tile0 = p.sp.tile0, v.sp.n = p.sp.n, v.sp.len = p.sp.len, v.sp.nl = p.sp.nl;
+}
+
 template <class F>
 struct Warp {
     // operands of the unit's query rows
@@ -225,13 +258,12 @@ struct Warp {
     float f[F::NT][F::RPL];      // base-2 score = f * what step() holds
     float scale[F::MOD ? F::NT : 1][F::RPL];
     float slope[F::MOD ? F::NT : 1][F::RPL];
-    int pos[F::NT][F::RPL];      // positions of the lane's rows
-    int minpos, maxpos;          // over the unit's rows that have one
+    int pos[F::MOD ? F::NT : 1][F::RPL];  // positions of the lane's rows
     // sums
     float o[F::NB][2][F::NT][4];
-    float ob[F::NT][F::NB][4];   // of the weights; SPLIT: not used
+    float ob[F::NT][F::NB][4];   // of the weights times value scales; SPLIT: not used
     float ref[F::NT][F::RPL], l[F::NT][F::RPL];
-    uint32_t top_scale;          // value scales are at most this power of two 2^E (binary16)
+    uint32_t top_scale;          // value scales are at most this power of two 2^E (binary16, twice)
     float lim;                   // 15 - E: weights are below 2^lim
 
     __device__ __forceinline__ void start() {
@@ -244,18 +276,18 @@ struct Warp {
 #pragma unroll
             for (int r = 0; r < F::RPL; ++r) ref[nt][r] = kNoRef, l[nt][r] = 0.0f;
         }
-        top_scale = F::SPLIT ? 0x0400u : 0x3c00u;
+        top_scale = F::SPLIT ? 0x04000400u : 0x3c003c00u;
         lim = F::SPLIT ? 29.0f : 15.0f;
     }
 
     // Loads the query rows of unit u of sequence s.
-    __device__ __forceinline__ void load_queries(const AttnParams& P, const Place& at, int rt_count, int group, int lane) {
+    __device__ __forceinline__ void load_queries(const AttnParams& P, const Place& at, volatile Held& held, int rt_count, int group, int lane) {
         const int g = lane >> 2, c = lane & 3;
         const int h = at.u / rt_count, rt = at.u - h * rt_count, rows = P.tokens * group;
         const int first = at.sp.len - at.sp.nl;
         const int last_row = min((rt + 1) * F::RC, rows) - 1;
-        minpos = max(first + rt * F::RC / group, 0);
-        maxpos = min(first + last_row / group, at.sp.len - 1);
+        held.minpos = max(first + rt * F::RC / group, 0);
+        held.maxpos = min(first + last_row / group, at.sp.len - 1);
 #pragma unroll
         for (int nt = 0; nt < F::NT; ++nt) {
             // column g of the tile: a row, or one of its two parts
@@ -331,11 +363,12 @@ struct Warp {
 #pragma unroll
             for (int r = 0; r < F::RPL; ++r) {
                 const float fr = __shfl_sync(kFull, fg, 8 * c + 4 * r);
-                const int mine = min(rt * F::RC + (nt * 4 + c) * F::RPL + r, rows - 1);
-                const RowAt ra = row_of(P, at.sp, h, group, mine);
-                pos[nt][r] = first + ra.i;
                 f[nt][r] = F::MOD ? kLog2e : fmaxf(fr * kLog2e, 0x1p-140f);  // not 0: -inf is to stay that
-                if (F::MOD) scale[nt][r] = fr, slope[nt][r] = P.alibi ? P.alibi[ra.hq] : 0.0f;
+                if (F::MOD) {
+                    const RowAt ra = row_of(P, at.sp, h, group, min(rt * F::RC + (nt * 4 + c) * F::RPL + r, rows - 1));
+                    pos[nt][r] = first + ra.i;
+                    scale[nt][r] = fr, slope[nt][r] = P.alibi ? P.alibi[ra.hq] : 0.0f;
+                }
             }
         }
     }
@@ -356,7 +389,7 @@ struct Warp {
 
     // Value scales up to the binary16 `dmax` come: weights get as many bits less.
     __device__ __forceinline__ void raise_scales(uint32_t dmax) {
-        const int E = (int)(top_scale >> 10) - 15;
+        const int E = (int)(top_scale >> 26) - 15;
         const int En = max(E, min(16, (int)(__reduce_max_sync(kFull, dmax) >> 10) - 14));
 #pragma unroll
         for (int nt = 0; nt < F::NT; ++nt) {
@@ -368,19 +401,22 @@ struct Warp {
             }
             rescale(nt, alpha);
         }
-        top_scale = (uint32_t)(En + 15) << 10;
+        top_scale = (uint32_t)(En + 15) * 0x04000400u;
         lim = (float)(15 - En);
     }
 
     // Scores s come that the references do not hold: rows with one move up to it.
-    __device__ __forceinline__ void raise_refs(const float (&s)[F::NT][F::VPT]) {
+    __device__ __forceinline__ void raise_refs(const float (&s)[2][F::NT][F::VPT]) {
 #pragma unroll
         for (int nt = 0; nt < F::NT; ++nt) {
             float alpha[F::RPL];
 #pragma unroll
             for (int r = 0; r < F::RPL; ++r) {
-                float m = s[nt][r] * f[nt][r];
-                m = fmaxf(m, s[nt][r + F::RPL] * f[nt][r]);
+                float m = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int v = r; v < F::VPT; v += F::RPL) m = fmaxf(m, s[u][nt][v] * f[nt][r]);
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
@@ -407,137 +443,104 @@ struct Warp {
         return *reinterpret_cast<const uint32_t*>(&h);
     }
 
-    // Sixteen tokens (u: the first or the second of a record) from position p0 on; edge:
-    // some (row, token) is masked (the same for the whole warp).
-    __device__ __forceinline__ void step(const AttnParams& P, const uint8_t* rec, int u, int p0, bool edge, int lane) {
+    // Scores of sixteen tokens (u: the first or the second of a record) from position p0 on.
+    __device__ __forceinline__ void scores(const AttnParams& P, const uint8_t* rec, int u, int p0, int lane, float (&s)[F::NT][F::VPT]) {
         constexpr int NB = F::NB, C = F::C, NT = F::NT, DIM = F::DIM;
         const int g = lane >> 2, c = lane & 3;
-        // scores
-        float s[NT][F::VPT];
-        {
-            float t[NT][4];
-            uint32_t ds[2][NB / 2];
-            load_words(rec + key_scale(DIM, 16 * u + g, 0), ds[0]);
-            load_words(rec + key_scale(DIM, 16 * u + g + 8, 0), ds[1]);
+        float t[NT][4];
+        uint32_t ds[2][NB / 2];
+        load_words(rec + key_scale(DIM, 16 * u + g, 0), ds[0]);
+        load_words(rec + key_scale(DIM, 16 * u + g + 8, 0), ds[1]);
+        if constexpr (F::SPLIT) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = 0.0f;
+        } else {
+            // word c (of NB / 2, going round) of the scales of tokens g and g + 8
+            const int at = 4 * (c % (NB / 2));
+            const uint32_t a0 = *reinterpret_cast<const uint32_t*>(rec + key_scale(DIM, 16 * u + g, 0) + at);
+            const uint32_t a1 = *reinterpret_cast<const uint32_t*>(rec + key_scale(DIM, 16 * u + g + 8, 0) + at);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v) t[nt][v] = 0.0f;
-            }
-            if constexpr (!F::SPLIT) {
-                // word c (of NB / 2, going round) of the scales of tokens g and g + 8
-                const int at = 4 * (c % (NB / 2));
-                const uint32_t a0 = *reinterpret_cast<const uint32_t*>(rec + key_scale(DIM, 16 * u + g, 0) + at);
-                const uint32_t a1 = *reinterpret_cast<const uint32_t*>(rec + key_scale(DIM, 16 * u + g + 8, 0) + at);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < (NB == 8 ? 2 : 1); ++i) mma8(t[nt], a0, a1, bias[nt][i]);
-            }
-#pragma unroll
-            for (int ch = 0; ch < F::NCH; ++ch) {
-                uint32_t w[2][C];
-                load_words(rec + key_word(DIM, 16 * u + g, ch * C, c), w[0]);
-                load_words(rec + key_word(DIM, 16 * u + g + 8, ch * C, c), w[1]);
-#pragma unroll
-                for (int bb = 0; bb < C; ++bb) {
-                    const int b = ch * C + bb;
-                    const float d0 = b & 1 ? half_hi(ds[0][b / 2]) : half_lo(ds[0][b / 2]);
-                    const float d1 = b & 1 ? half_hi(ds[1][b / 2]) : half_lo(ds[1][b / 2]);
-                    const uint32_t w0 = w[0][bb], w1 = w[1][bb], y0 = w0 >> 8, y1 = w1 >> 8;
-                    const uint32_t a[8] = {low(w0), low(w1), high(w0), high(w1), low(y0), low(y1), high(y0), high(y1)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float z[4];
-                        mma(z, a[0], a[1], a[2], a[3], qb[nt][b][0], qb[nt][b][1], 0.0f, 0.0f, 0.0f, 0.0f);
-                        mma(z, a[4], a[5], a[6], a[7], qb[nt][b][2], qb[nt][b][3], z[0], z[1], z[2], z[3]);
-                        if constexpr (F::SPLIT) {
-                            t[nt][0] = fmaf(d0, z[0] + z[1], t[nt][0]);
-                            t[nt][1] = fmaf(d1, z[2] + z[3], t[nt][1]);
-                        } else {
-                            t[nt][0] = fmaf(d0, z[0], t[nt][0]);
-                            t[nt][1] = fmaf(d0, z[1], t[nt][1]);
-                            t[nt][2] = fmaf(d1, z[2], t[nt][2]);
-                            t[nt][3] = fmaf(d1, z[3], t[nt][3]);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int v = 0; v < F::VPT; ++v) {
-                    const int r = v % F::RPL, key = p0 + g + 8 * (v / F::RPL);
-                    float x = t[nt][v];
-                    if (F::MOD) {
-                        x *= scale[nt][r];
-                        if (P.softcap > 0.0f) x = P.softcap * tanhf(x / P.softcap);
-                        x = fmaf(slope[nt][r], (float)(key - pos[nt][r]), x);
-                    }
-                    s[nt][v] = x;
-                }
-            if (edge) {
-                const int window = P.window > 0 ? P.window : kNoWindow;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int v = 0; v < F::VPT; ++v) {
-                        const int r = v % F::RPL, key = p0 + g + 8 * (v / F::RPL);
-                        if (key > pos[nt][r] || key <= pos[nt][r] - window) s[nt][v] = -INFINITY;
-                    }
+                mma8(t[nt], a0, a1, bias[nt][0], 0.0f, 0.0f, 0.0f, 0.0f);
+                if (NB == 8) mma8(t[nt], a0, a1, bias[nt][F::NB == 8], t[nt][0], t[nt][1], t[nt][2], t[nt][3]);
             }
         }
-        float y[NT][F::VPT], top = -INFINITY;
+#pragma unroll
+        for (int ch = 0; ch < F::NCH; ++ch) {
+            uint32_t w[2][C];
+            load_words(rec + key_word(DIM, 16 * u + g, ch * C, c), w[0]);
+            load_words(rec + key_word(DIM, 16 * u + g + 8, ch * C, c), w[1]);
+#pragma unroll
+            for (int bb = 0; bb < C; ++bb) {
+                const int b = ch * C + bb;
+                const float d0 = b & 1 ? half_hi(ds[0][b / 2]) : half_lo(ds[0][b / 2]);
+                const float d1 = b & 1 ? half_hi(ds[1][b / 2]) : half_lo(ds[1][b / 2]);
+                const uint32_t w0 = w[0][bb], w1 = w[1][bb], y0 = w0 >> 8, y1 = w1 >> 8;
+                const uint32_t a[8] = {low(w0), low(w1), high(w0), high(w1), low(y0), low(y1), high(y0), high(y1)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float z[4];
+                    mma(z, a[0], a[1], a[2], a[3], qb[nt][b][0], qb[nt][b][1], 0.0f, 0.0f, 0.0f, 0.0f);
+                    mma(z, a[4], a[5], a[6], a[7], qb[nt][b][2], qb[nt][b][3], z[0], z[1], z[2], z[3]);
+                    if constexpr (F::SPLIT) {
+                        t[nt][0] = fmaf(d0, z[0] + z[1], t[nt][0]);
+                        t[nt][1] = fmaf(d1, z[2] + z[3], t[nt][1]);
+                    } else {
+                        t[nt][0] = fmaf(d0, z[0], t[nt][0]);
+                        t[nt][1] = fmaf(d0, z[1], t[nt][1]);
+                        t[nt][2] = fmaf(d1, z[2], t[nt][2]);
+                        t[nt][3] = fmaf(d1, z[3], t[nt][3]);
+                    }
+                }
+            }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int v = 0; v < F::VPT; ++v) {
-                y[nt][v] = fmaf(s[nt][v], f[nt][v % F::RPL], -ref[nt][v % F::RPL]);
-                top = fmaxf(top, y[nt][v]);
+                const int r = v % F::RPL, key = p0 + g + 8 * (v / F::RPL);
+                float x = t[nt][v];
+                if (F::MOD) {
+                    x *= scale[nt][r];
+                    if (P.softcap > 0.0f) x = P.softcap * tanhf(x / P.softcap);
+                    x = fmaf(slope[nt][r], (float)(key - pos[nt][r]), x);
+                }
+                s[nt][v] = x;
             }
-        if (__any_sync(kFull, top > lim)) {
-            raise_refs(s);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int v = 0; v < F::VPT; ++v) y[nt][v] = fmaf(s[nt][v], f[nt][v % F::RPL], -ref[nt][v % F::RPL]);
-        }
-        // weights times value scales, as B operands
+    }
+
+    // Adds the sixteen tokens' values, weighted by 2^y; s tells what is masked.
+    __device__ __forceinline__ void values(const uint8_t* rec, int u, bool edge, int lane, const float (&s)[F::NT][F::VPT],
+                                           const float (&y)[F::NT][F::VPT]) {
+        constexpr int NB = F::NB, C = F::C, NT = F::NT, DIM = F::DIM;
+        const int g = lane >> 2, c = lane & 3;
+        // weights times value scales: in the scores' layout (token g or g + 8 of the lane, its
+        // columns), then turned into B operands
         uint32_t pb[NT][NB][2];
-        if constexpr (F::SPLIT) {
+        {
             uint32_t dv[2][NB / 2];
             load_words(rec + value_scale(DIM, 16 * u + g, 0), dv[0]);
             load_words(rec + value_scale(DIM, 16 * u + g + 8, 0), dv[1]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const float p = ex2(y[nt][v]);
-                    l[nt][0] += p;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const float q = p * (b & 1 ? half_hi(dv[v][b / 2]) : half_lo(dv[v][b / 2]));
-                        const float hi = __uint_as_float(__float_as_uint(q) & 0xffffe000u);
-                        pb[nt][b][v] = transposed(pack_half2(hi, q - hi));
-                    }
-                }
-        } else {
-            uint32_t dv[2][2][NB / 2];  // [8 j][token 2 c + e]
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                load_words(rec + value_scale(DIM, 16 * u + 8 * j + 2 * c, 0), dv[j][0]);
-                load_words(rec + value_scale(DIM, 16 * u + 8 * j + 2 * c + 1, 0), dv[j][1]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float p0_ = ex2(y[nt][2 * j]), p1_ = ex2(y[nt][2 * j + 1]);
-                    l[nt][0] += p0_, l[nt][F::RPL - 1] += p1_;
-                    const uint32_t pt = transposed(pack_half2(p0_, p1_));
+                    if constexpr (F::SPLIT) {
+                        const float p = ex2(y[nt][j]);
+                        l[nt][0] += p;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        pb[nt][b][j] = mul_half2(pt, __byte_perm(dv[j][0][b / 2], dv[j][1][b / 2], b & 1 ? 0x7632 : 0x5410));
+                        for (int b = 0; b < NB; ++b) {
+                            const float q = p * (b & 1 ? half_hi(dv[j][b / 2]) : half_lo(dv[j][b / 2]));
+                            const float hi = __uint_as_float(__float_as_uint(q) & 0xffffe000u);
+                            pb[nt][b][j] = pack_half2(hi, q - hi);
+                        }
+                    } else {
+                        const float p = ex2(y[nt][2 * j]), q = ex2(y[nt][2 * j + 1]);
+                        l[nt][0] += p, l[nt][F::RPL - 1] += q;
+                        const uint32_t w = pack_half2(p, q);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) pb[nt][b][j] = mul_half2(w, b & 1 ? both_high(dv[j][b / 2]) : both_low(dv[j][b / 2]));
+                    }
                 }
         }
         // a masked token's weight is 0 whatever its scale is, NaN too
@@ -546,14 +549,16 @@ struct Warp {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float a = s[nt][F::RPL * j] == -INFINITY ? 0.0f : 1.0f;
-                    const float z = s[nt][F::RPL * j + F::RPL - 1] == -INFINITY ? 0.0f : 1.0f;
-                    const uint32_t keep = nonzero_half2(transposed(pack_half2(a, z)));
+                    const uint32_t keep = (s[nt][F::RPL * j] == -INFINITY ? 0u : 0xffffu) |
+                                          (s[nt][F::RPL * j + F::RPL - 1] == -INFINITY ? 0u : 0xffff0000u);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) pb[nt][b][j] &= keep;
                 }
         }
-        // values
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) pb[nt][b][0] = transposed(pb[nt][b][0]), pb[nt][b][1] = transposed(pb[nt][b][1]);
 #pragma unroll
         for (int ch = 0; ch < F::NCH; ++ch) {
             uint32_t w[2][C];  // token pairs 2c, 2c + 1 and 8 behind: [e][C halves]
@@ -581,20 +586,63 @@ struct Warp {
         }
     }
 
-    // One record of 32 tokens from position p0 on.
-    __device__ __forceinline__ void tile(const AttnParams& P, const uint8_t* rec, int p0, int lane) {
+    // Masks the scores of a record from position p0 on.
+    __device__ __forceinline__ void mask(const AttnParams& P, const volatile Held& held, int p0, int lane, float (&s)[2][F::NT][F::VPT]) {
+        const int g = lane >> 2, c = lane & 3;
         const int window = P.window > 0 ? P.window : kNoWindow;
+        const int group = P.q_heads / P.cache.heads, rows = P.tokens * group, rt_count = (rows + F::RC - 1) / F::RC;
+        const int row0 = held.at.u % rt_count * F::RC + c * F::RPL, first = held.at.sp.len - held.at.sp.nl;
+#pragma unroll
+        for (int nt = 0; nt < F::NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < F::RPL; ++r) {
+                const int at = first + min(row0 + nt * F::RPL * 4 + r, rows - 1) / group;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int v = r; v < F::VPT; v += F::RPL) {
+                        const int key = p0 + 16 * u + g + 8 * (v / F::RPL);
+                        if (key > at || key <= at - window) s[u][nt][v] = -INFINITY;
+                    }
+            }
+    }
+
+    // One record of 32 tokens from position p0 on.
+    __device__ __forceinline__ void tile(const AttnParams& P, const volatile Held& held, const uint8_t* rec, int p0, int lane) {
+        // edge: some (row, token) is masked (the same for the whole warp)
+        const int window = P.window > 0 ? P.window : kNoWindow, minpos = held.minpos, maxpos = held.maxpos;
         const bool edge = p0 + kGroup - 1 > minpos || p0 <= maxpos - window;
         uint32_t dv[F::NB / 2];
         load_words(rec + value_scale(F::DIM, lane, 0), dv);
-        uint32_t m = abs_half2(dv[0]);
+        uint32_t top_d = dv[0] & 0x7fff7fffu;
 #pragma unroll
-        for (int i = 1; i < F::NB / 2; ++i) m = max_half2(m, abs_half2(dv[i]));
-        m = max(m & 0xffffu, m >> 16);
-        if (edge && (p0 + lane > maxpos || p0 + lane <= minpos - window)) m = 0;
-        if (__any_sync(kFull, m > top_scale)) raise_scales(m);
-#pragma unroll 1
-        for (int u = 0; u < 2; ++u) step(P, rec, u, p0 + 16 * u, edge, lane);
+        for (int i = 1; i < F::NB / 2; ++i) top_d = max_half2(top_d, dv[i] & 0x7fff7fffu);
+        float s[2][F::NT][F::VPT], y[2][F::NT][F::VPT], top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) scores(P, rec, u, p0 + 16 * u, lane, s[u]);
+        if (edge) {
+            mask(P, held, p0, lane, s);
+            if (p0 + lane > maxpos || p0 + lane <= minpos - window) top_d = 0;
+        }
+        auto exponents = [&] {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < F::NT; ++nt)
+#pragma unroll
+                    for (int v = 0; v < F::VPT; ++v) {
+                        y[u][nt][v] = fmaf(s[u][nt][v], f[nt][v % F::RPL], -ref[nt][v % F::RPL]);
+                        top = fmaxf(top, y[u][nt][v]);
+                    }
+        };
+        exponents();
+        if (__any_sync(kFull, top > lim || !within_half2(top_d, top_scale))) {
+            if (!__all_sync(kFull, within_half2(top_d, top_scale))) raise_scales(max(top_d & 0xffffu, top_d >> 16));
+            raise_refs(s);
+            exponents();
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) values(rec, u, edge, lane, s[u], y[u]);
     }
 
     // For each row of the lane, begin(row of the unit, ref, l) and pair(what that returned,
@@ -631,48 +679,39 @@ struct Producer {
     const uint8_t* from;  // the next record
     int run;              // records behind it in the page that the warp reads, itself included
     int left;             // tiles not yet issued
-    uint32_t filled;      // per stage: a copy was issued into it
+    int entry;            // lane i holds entry held.base + i of the table's row
+    uint32_t filled;      // bit i: a copy was issued for the i-th tile from the one to be used next
     bool good;            // the page exists
-    // looked at where a page or a unit ends
-    int page, base, entry;  // ordinal of the page in the sequence's table; lane i holds entry base + i
-    int unit_left;          // records of the unit behind this page
-    Place at;
 
-    __device__ __forceinline__ void load_entries(const AttnParams& P, int lane) {
-        base = page;
+    __device__ __forceinline__ void load_entries(const AttnParams& P, int s, int base, int lane) {
         const int i = base + lane;
-        entry = i < P.seqs.table_pages ? P.seqs.table[at.s * P.seqs.table_stride + i] : -1;
+        entry = i < P.seqs.table_pages ? P.seqs.table[s * P.seqs.table_stride + i] : -1;
     }
-    // From record r of the page on.
-    __device__ __forceinline__ void open(const AttnParams& P, int rt_count, int r, int lane) {
+    // From record r of a page on; `unit` of the unit's records are left.
+    __device__ __forceinline__ void open(const AttnParams& P, volatile Held& held, const Place& at, int rt_count, int page, int base, int r, int unit, int lane) {
         const int rpp = P.cache.page_size / kGroup;
         const int pg = __shfl_sync(kFull, entry, page - base);
         good = (uint32_t)pg < (uint32_t)P.cache.pages && !nothing(at.sp);
         if (!good && !nothing(at.sp) && lane == 0) atomicOr(P.ws, kBadPage);
         const int h = rt_count == 1 ? at.u : at.u / rt_count;
         from = P.cache.data + (((int64_t)pg * P.cache.heads + h) * rpp + r) * F::REC;
-        run = min(rpp - r, unit_left);
-        unit_left -= run;
+        run = min(rpp - r, unit);
+        held.page = page, held.base = base, held.unit_left = unit - run;
     }
-    __device__ __forceinline__ void seek(const AttnParams& P, int rt_count, int lane) {
-        const int rpp = P.cache.page_size / kGroup, tile = at.sp.tile0 + at.t;
-        page = tile / rpp;
-        unit_left = at.sp.n - at.t;
-        load_entries(P, lane);
-        open(P, rt_count, tile - page * rpp, lane);
+    __device__ __forceinline__ void seek(const AttnParams& P, volatile Held& held, const Place& at, int rt_count, int lane) {
+        const int rpp = P.cache.page_size / kGroup, tile = at.sp.tile0 + at.t, page = tile / rpp;
+        put(held.next, at);
+        load_entries(P, at.s, page, lane);
+        open(P, held, at, rt_count, page, page, tile - page * rpp, at.sp.n - at.t, lane);
     }
-    __device__ __forceinline__ void start(const AttnParams& P, const Place& place, int tiles, int rt_count, int lane) {
-        at = place;
+    __device__ __forceinline__ void start(const AttnParams& P, volatile Held& held, const Place& place, int tiles, int rt_count, int lane) {
         left = tiles;
         filled = 0;
-        seek(P, rt_count, lane);
+        seek(P, held, place, rt_count, lane);
     }
-    __device__ __forceinline__ void issue(const AttnParams& P, int units, int rt_count, uint8_t* slot, uint64_t* bar, int stage, int lane) {
-        if (left == 0) {
-            filled &= ~(1u << stage);
-            return;
-        }
-        filled = good ? filled | 1u << stage : filled & ~(1u << stage);
+    __device__ __forceinline__ void issue(const AttnParams& P, volatile Held& held, int units, int rt_count, uint8_t* slot, uint64_t* bar, uint32_t bit, int lane) {
+        if (left == 0) return;
+        if (good) filled |= bit;
         if (good && lane == 0) {
             q4dev::mbar_arrive_expect_tx(bar, F::REC);
             q4dev::bulk_g2s(slot, from, F::REC, bar);
@@ -680,16 +719,20 @@ struct Producer {
         from += F::REC;
         --left;
         if (--run == 0 && left > 0) {
-            if (unit_left > 0) {
-                if (++page - base == 32) load_entries(P, lane);
-                open(P, rt_count, 0, lane);
+            Place at = get(held.next);
+            const int unit = held.unit_left;
+            if (unit > 0) {
+                const int page = held.page + 1;
+                int base = held.base;
+                if (page - base == 32) load_entries(P, at.s, base = page, lane);
+                open(P, held, at, rt_count, page, base, 0, unit, lane);
             } else {
                 at.t = 0;
                 if (++at.u == units) {
                     at.u = 0;
                     at.sp = span_at(P, ++at.s);
                 }
-                seek(P, rt_count, lane);
+                seek(P, held, at, rt_count, lane);
             }
         }
     }
@@ -790,6 +833,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + F::OFF_BAR) + warp * F::STAGES;
     int64_t* const pre = reinterpret_cast<int64_t*>(smem + F::OFF_PRE);
     uint8_t* const ring = smem + warp * F::RING;
+    volatile Held& held = reinterpret_cast<Held*>(smem + F::OFF_HELD)[warp];
 
     const int group = P.q_heads / P.cache.heads;
     const int rows = P.tokens * group, rt_count = (rows + F::RC - 1) / F::RC;
@@ -853,9 +897,8 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
 
     if (todo > 0) {
         // the place of tile wa
-        Place at;
-        int64_t start;  // first tile of the unit
         {
+            Place at;
             const int64_t y = units == 1 ? wa : quotient(wa, units);
             int64_t rest;
             if (few) {
@@ -885,42 +928,49 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
             const int64_t off = wa - (y - rest) * units;
             at.u = units == 1 ? 0 : (int)quotient(off, at.sp.n);
             at.t = (int)(off - (int64_t)at.u * at.sp.n);
-            start = wa - at.t;
+            held.start = wa - at.t;
+            put(held.at, at);
         }
         Producer<F> prod;
-        prod.start(P, at, todo, rt_count, lane);
+        prod.start(P, held, get(held.at), todo, rt_count, lane);
 #pragma unroll
-        for (int i = 0; i < F::STAGES; ++i) prod.issue(P, units, rt_count, ring + i * F::REC, bars + i, i, lane);
+        for (int i = 0; i < F::STAGES; ++i) prod.issue(P, held, units, rt_count, ring + i * F::REC, bars + i, 1u << i, lane);
 
         Warp<F> w;
-        int stage = 0;
-        uint32_t phases = 0;
+        uint32_t used = 0, phases = 0;  // tiles done; bit i: parity of the next wait on stage i
         bool dead = false;
         while (todo > 0) {
-            const int n = min(at.sp.n - at.t, todo);
-            const bool whole = n == at.sp.n, empty = nothing(at.sp);
-            if (!empty) {
-                w.load_queries(P, at, rt_count, group, lane);
-                w.start();
+            int n, p0;
+            {
+                const Place at = get(held.at);
+                n = min(at.sp.n - at.t, todo);
+                p0 = (at.sp.tile0 + at.t) * kGroup;
+                if (!nothing(at.sp)) {
+                    w.load_queries(P, at, held, rt_count, group, lane);
+                    w.start();
+                }
             }
-            int p0 = (at.sp.tile0 + at.t) * kGroup;
-            for (int i = 0; i < n; ++i) {
-                if (prod.filled >> stage & 1) {
+            for (int i = n; i > 0; --i) {
+                const uint32_t stage = used % F::STAGES;
+                uint8_t* const slot = ring + stage * F::REC;
+                if (prod.filled & 1) {
                     // after a wait that gave up nothing is issued or computed any more, and the
                     // copies in flight are still waited for
                     if (!__all_sync(kFull, q4dev::mbar_wait_short_bounded(bars + stage, phases >> stage & 1))) dead = true;
                     phases ^= 1u << stage;
-                    if (dead) {
+                    if (dead)
                         prod.left = 0;
-                    } else {
-                        w.tile(P, ring + stage * F::REC, p0, lane);
-                    }
+                    else
+                        w.tile(P, held, slot, p0, lane);
                 }
                 __syncwarp();
-                prod.issue(P, units, rt_count, ring + stage * F::REC, bars + stage, stage, lane);
-                stage = stage + 1 == F::STAGES ? 0 : stage + 1;
+                prod.filled >>= 1;
+                prod.issue(P, held, units, rt_count, slot, bars + stage, 1u << (F::STAGES - 1), lane);
+                ++used;
                 p0 += kGroup;
             }
+            Place at = get(held.at);
+            const bool whole = n == at.sp.n, empty = nothing(at.sp);
             todo -= n;
             const int h = rt_count == 1 ? at.u : at.u / rt_count, row0 = (at.u - h * rt_count) * F::RC;
             if (empty) {
@@ -954,17 +1004,18 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                     [&](float* to, int x, float v0, float v1) { *reinterpret_cast<float2*>(to + x) = make_float2(v0, v1); });
                 if (lane == 0) {
                     Entry& e = ents[2 * warp + last];
-                    e.start = start, e.s = at.s, e.u = at.u, e.n = at.sp.n;
+                    e.start = held.start, e.s = at.s, e.u = at.u, e.n = at.sp.n;
                     e.part = (int)(p - reinterpret_cast<float*>(smem));
                 }
             }
-            start += at.sp.n;
             if (todo > 0) {
+                held.start = held.start + at.sp.n;
                 at.t = 0;
                 if (++at.u == units) {
                     at.u = 0;
                     at.sp = span_at(P, ++at.s);
                 }
+                put(held.at, at);
             }
         }
         if (dead && lane == 0) atomicOr(P.ws, kTimeoutFlag);
