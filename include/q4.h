@@ -347,8 +347,10 @@ size_t q4_kv_attention_workspace_bytes(int32_t dim);
  * (q4_workspace_status) becomes Q4_ERR_INVALID_ARG until it is zeroed. lens above the
  * table's reach count as that.
  * Scores, softmax and sums are binary32; see the kernel for what is rounded to fewer bits.
- * Errors: as q4_kv_write, Q4_ERR_WORKSPACE, and Q4_ERR_UNSUPPORTED for tokens outside
- * 0..16. */
+ * Errors: as q4_kv_write, Q4_ERR_WORKSPACE, Q4_ERR_UNSUPPORTED for tokens outside 0..16, and
+ * Q4_ERR_INVALID_ARG for more than 4096 query heads a key/value head or for tables that could
+ * hold too much: with u = heads * ceil(tokens * q_heads / heads / 4),
+ * count * table_pages * (page_size / 32) * u has to be below 2^31. */
 q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
                           const q4_rows* q, const q4_kv_scores* scores, const q4_rows* out, float* lse,
                           void* ws, size_t ws_bytes, void* stream);

@@ -661,7 +661,8 @@ int q4_debug_check_kv_plan(const int32_t* lens, const int32_t* new_lens, int cou
         }
         before[s + 1] = before[s] + sp[s].n;
     }
-    const int64_t total = before[count] * units;
+    if (before[count] * units > INT32_MAX) return 15;  // the host refuses the call
+    const int total = (int)(before[count] * units);
     const int ctas = ctas_of(total, units, count, warps, grid);
     const Parts parts(total, ctas);
     if (ctas < 1 || ctas > grid) return 5;
@@ -670,9 +671,9 @@ int q4_debug_check_kv_plan(const int32_t* lens, const int32_t* new_lens, int cou
     int s = 0;  // sequence of `next`
     for (int i = 0; i < ctas; ++i) {
         const int64_t a = parts.begin(i), z = parts.begin(i + 1);
-        if (a != next || z <= a || parts.of(a) != i || parts.of(z - 1) != i) return 6;
+        if (a != next || z <= a || parts.of((int)a) != i || parts.of((int)z - 1) != i) return 6;
         int64_t w_next = a;
-        const Parts wp(z - a, warps);
+        const Parts wp((int)(z - a), warps);
         for (int w = 0; w < warps; ++w) {
             const int64_t wa = a + wp.begin(w), wz = a + wp.begin(w + 1);
             if (wa != w_next || wz < wa || wz > z) return 7;
@@ -684,7 +685,7 @@ int q4_debug_check_kv_plan(const int32_t* lens, const int32_t* new_lens, int cou
             while (x >= before[s + 1] * units) ++s;
             const int64_t off = x - before[s] * units, start = before[s] * units + off / sp[s].n * sp[s].n, end = start + sp[s].n;
             if (start < a || end > z) {
-                const int slot = start > a, i0 = parts.of(start), i1 = parts.of(end - 1);
+                const int slot = start > a, i0 = parts.of((int)start), i1 = parts.of((int)end - 1);
                 if (i0 > i || i1 < i || i0 == i1) return 9;
                 if (slot_used[2 * i + slot]++) return 10;
                 // the slot in which the joining CTA looks

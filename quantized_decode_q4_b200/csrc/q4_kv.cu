@@ -55,10 +55,6 @@ __device__ __forceinline__ uint8_t* record(const MoveParams& P, int s, int h, in
     return P.cache.data + record_at(P.cache, DIM, page, h, p - pg * P.cache.page_size);
 }
 
-// The types of a call's rows: one of q4_dtype where keys and values both have it and four
-// neighbours can be moved at once, else anything, looked up at each access.
-constexpr int kAnyRows = 3;
-
 __device__ __forceinline__ uint32_t max8(uint32_t v) {
 #pragma unroll
     for (int off = 1; off < 8; off <<= 1) v = max(v, __shfl_xor_sync(kFull, v, off));
@@ -118,25 +114,6 @@ __device__ __forceinline__ void quantise(const float (&v)[4], int i8, uint32_t* 
     const uint32_t o = __shfl_xor_sync(kFull, w, 4);
     *word = (i8 < 4 ? o : w) * 16 + (i8 < 4 ? w : o);
     *d = top >= 0x7f800000u ? (uint16_t)0x7fffu : __half_as_ushort(__float2half_rn(dd));
-}
-
-template <int T>
-__device__ __forceinline__ void load_four(const Rows& r, int64_t at, float (&v)[4]) {
-    if constexpr (T == kAnyRows) {
-        load4(r, at, v);
-    } else if constexpr (T == Q4_F32) {
-        const float4 t = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(r.data) + at));
-        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-    } else {
-        const uint2 t = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(r.data) + at));
-        if constexpr (T == Q4_BF16) {
-            v[0] = __uint_as_float(t.x << 16), v[1] = __uint_as_float(t.x & 0xffff0000u);
-            v[2] = __uint_as_float(t.y << 16), v[3] = __uint_as_float(t.y & 0xffff0000u);
-        } else {
-            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&t.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&t.y));
-            v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-        }
-    }
 }
 
 // Where the lane's parts of a token go: for the chunk that holds block bb.

@@ -114,8 +114,11 @@ q4_status q4_kv_read(const q4_kv_cache* cache, const q4_kv_seqs* seqs, const int
 }
 
 size_t q4_kv_attention_workspace_bytes(int32_t dim) {
-    if (dim != 64 && dim != 128 && dim != 256) return 0;
-    return (size_t)kHeaderBytes + 4 * q4kv::kv_attention_part_floats(dim);
+    const size_t floats = dim == 64    ? q4kv::kv_attention_part_floats<64>()
+                          : dim == 128 ? q4kv::kv_attention_part_floats<128>()
+                          : dim == 256 ? q4kv::kv_attention_part_floats<256>()
+                                       : 0;
+    return floats ? (size_t)kHeaderBytes + 4 * floats : 0;
 }
 
 q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
@@ -125,7 +128,13 @@ q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int3
     if (s != Q4_OK) return s;
     if ((s = check_seqs(cache, seqs)) != Q4_OK) return s;
     if (tokens < 0 || tokens > Q4_MAX_BATCH) return Q4_ERR_UNSUPPORTED;
-    if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads) return Q4_ERR_INVALID_ARG;
+    if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads || q_heads / cache->heads > 4096) return Q4_ERR_INVALID_ARG;
+    {
+        // tiles that the tables could hold, four query rows a unit at least: counted in 31 bits
+        const int64_t units = (int64_t)cache->heads * ((tokens * (q_heads / cache->heads) + 3) / 4);
+        const int64_t each = (int64_t)seqs->table_pages * (cache->page_size / q4kv::kGroup) * units;
+        if (seqs->count > 0 && each > INT32_MAX / seqs->count) return Q4_ERR_INVALID_ARG;
+    }
     if (!scores || !std::isfinite(scores->scale) || !(scores->scale > 0.0f)) return Q4_ERR_INVALID_ARG;
     if (!std::isfinite(scores->softcap) || scores->softcap < 0.0f || scores->window < 0) return Q4_ERR_INVALID_ARG;
     if ((s = check_rows(q, seqs->count, tokens, q_heads, cache->dim, false)) != Q4_OK) return s;
@@ -150,9 +159,14 @@ q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int3
     P.window = scores->window;
     P.tokens = tokens;
     P.q_heads = q_heads;
-    if (cuda_failed(q4kv::launch_kv_attention(cache->dim, P, num_sms,
-                                              static_cast<cudaStream_t>(stream))))
-        return Q4_ERR_CUDA;
+    P.group = q_heads / cache->heads;
+    P.rows = tokens * P.group;
+    P.group_inv = P.group == 1 ? 0u : (uint32_t)(((UINT64_C(1) << 32) + P.group - 1) / P.group);
+    P.rpp = cache->page_size / q4kv::kGroup;
+    auto* const launch = cache->dim == 64    ? q4kv::launch_kv_attention<64>
+                         : cache->dim == 128 ? q4kv::launch_kv_attention<128>
+                                             : q4kv::launch_kv_attention<256>;
+    if (cuda_failed(launch(P, num_sms, static_cast<cudaStream_t>(stream)))) return Q4_ERR_CUDA;
     count_launches(1);
     return Q4_OK;
 }

@@ -29,6 +29,8 @@
 // 2^-11 twice, an eighth of the result's own last place... each).
 //
 // One CTA an SM; each warp streams its own tiles through its own ring of records.
+#pragma once
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -53,10 +55,11 @@ constexpr int kJoin = 16;  // chunks of parts in a join; 16 parts each hold all 
 constexpr float kNoRef = -1e30f;  // reference of a row that has seen nothing: finite, so that masked scores give weights of 0
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <int DIM_, int NT_, bool SPLIT_, bool MOD_>
+// T: the type of queries and results, or kAnyRows, kAnyBf16; MOD: scores are capped or biased.
+template <int DIM_, int NT_, int T_, bool MOD_>
 struct Cfg {
-    static constexpr int DIM = DIM_, NT = NT_;
-    static constexpr bool SPLIT = SPLIT_, MOD = MOD_;
+    static constexpr int DIM = DIM_, NT = NT_, T = T_;
+    static constexpr bool SPLIT = T != Q4_BF16 && T != kAnyBf16, MOD = MOD_;
     static constexpr int NB = DIM / 32, C = chunk_blocks(DIM), NCH = NB / C;
     static constexpr int RPL = SPLIT ? 1 : 2;       // rows of a lane in a column tile
     static constexpr int RC = NT * RPL * 4;         // query rows of a unit
@@ -87,10 +90,10 @@ struct Cfg {
 
 // A part of a unit whose rows another warp has to see: where its sums lie.
 struct Entry {
-    int64_t start;  // first tile of the unit
-    int32_t s, u, n;
-    int32_t part;   // float offset in shared memory, -1: none
-    int32_t pad[2];
+    int32_t start, n;      // first tile of the unit, its tiles
+    int32_t s, h, row0;    // its sequence, key/value head and first row
+    int32_t len, nl;       // of the sequence
+    int32_t part;          // float offset in shared memory, -1: none
 };
 static_assert(sizeof(Entry) == 32, "entry");
 static_assert(16 * kJoin >= kMaxCtas, "chunks");
@@ -172,45 +175,26 @@ __device__ __forceinline__ Span span_at(const AttnParams& P, int s) {
     return span_of(P.seqs.lens[s], P.seqs.new_lens ? P.seqs.new_lens[s] : P.tokens, P.tokens, P.window, reach(P.cache, P.seqs));
 }
 
-__device__ __forceinline__ void store2(const Rows& r, int64_t at, float a, float b) {
-    if (r.type == Q4_F32) {
-        float* p = static_cast<float*>(r.data) + at;
-        if (r.vec)
-            *reinterpret_cast<float2*>(p) = make_float2(a, b);
-        else
-            p[0] = a, p[1] = b;
-        return;
-    }
-    uint16_t* p = static_cast<uint16_t*>(r.data) + at;
-    const uint32_t x = as_bits16(a, r.type == Q4_BF16), y = as_bits16(b, r.type == Q4_BF16);
-    if (r.vec)
-        *reinterpret_cast<uint32_t*>(p) = x | (y << 16);
-    else
-        p[0] = (uint16_t)x, p[1] = (uint16_t)y;
-}
+// The token of row `row` (0 .. rows - 1) of a key/value head.
+__device__ __forceinline__ int token_of(const AttnParams& P, int row) { return P.group_inv ? (int)__umulhi((uint32_t)row, P.group_inv) : row; }
 
-// Row `row` (0 .. tokens * group - 1) of key/value head h of sequence s: its token and query
-// head, and whether it has a position.
+// Where a row goes: its token and query head, the element of the output, and whether the
+// token has a position.
 struct RowAt {
     int i, hq;
     bool real;
 };
-__device__ __forceinline__ RowAt row_of(const AttnParams& P, const Span& sp, int h, int group, int row) {
+__device__ __forceinline__ RowAt row_of(const AttnParams& P, int len, int nl, int h, int row) {
     RowAt r;
-    r.i = row / group;
-    r.hq = h * group + (row - r.i * group);
-    r.real = r.i < sp.nl && sp.len - sp.nl + r.i >= 0;
+    r.i = token_of(P, row);
+    r.hq = h * P.group + (row - r.i * P.group);
+    r.real = r.i < nl && len - nl + r.i >= 0;
     return r;
 }
 
-// Where a row's result goes and what its sums are multiplied with.
-struct RowOut {
-    int64_t at;
-    float inv;
-};
-__device__ __forceinline__ RowOut row_out(const AttnParams& P, int s, const RowAt& r, float l) {
-    return {row_at(P.out, s, r.i, r.hq), l == 0.0f || !r.real ? 0.0f : 1.0f / l};
-}
+// What a row's sums are multiplied with; 0 for a row that sees nothing.
+__device__ __forceinline__ float inverse(const RowAt& r, float l) { return l == 0.0f || !r.real ? 0.0f : __frcp_rn(l); }
+
 __device__ __forceinline__ void write_lse(const AttnParams& P, int s, const RowAt& r, float m, float l) {
     if (P.lse) P.lse[((int64_t)s * P.tokens + r.i) * P.q_heads + r.hq] = l == 0.0f || !r.real ? -INFINITY : (m + log2f(l)) * kLn2;
 }
@@ -220,16 +204,16 @@ __device__ __forceinline__ float result(float sum, float inv) { return inv == 0.
 // exp2(a - b) for a <= b, 1 where both are infinite.
 __device__ __forceinline__ float weight(float a, float b) { return a == b ? 1.0f : ex2(a - b); }
 
-// The warp's place in the work: unit u of sequence s, tile t of its span.
+// The warp's place in the work: key/value head h and row tile rt of sequence s, tile t of its span.
 struct Place {
-    int s, u, t;
+    int s, h, rt, t;
     Span sp;
 };
 
 // What a warp looks at where a page, a unit or a sequence ends is held in shared memory: its
 // loop needs the registers. Every lane writes and reads the same values.
 struct Held {
-    int64_t start;             // first tile of the unit that the warp works on
+    int start;                 // first tile of the unit that the warp works on
     Place at;                  // and its place
     Place next;                // of the next record to be copied
     int page, base;            // ordinal of its page in the sequence's table; lane i of the producer holds entry base + i
@@ -241,13 +225,23 @@ static_assert(sizeof(Held) <= 112, "held");
 
 __device__ __forceinline__ Place get(const volatile Place& v) {
     Place p;
-    p.s = v.s, p.u = v.u, p.t = v.t;
+    p.s = v.s, p.h = v.h, p.rt = v.rt, p.t = v.t;
     p.sp.tile0 = v.sp.tile0, p.sp.n = v.sp.n, p.sp.len = v.sp.len, p.sp.nl = v.sp.nl;
     return p;
 }
 __device__ __forceinline__ void put(volatile Place& v, const Place& p) {
-    v.s = p.s, v.u = p.u, v.t = p.t;
+    v.s = p.s, v.h = p.h, v.rt = p.rt, v.t = p.t;
     v.sp.tile0 = p.sp.tile0, v.sp.n = p.sp.n, v.sp.len = p.sp.len, v.sp.nl = p.sp.nl;
+}
+
+// The start of the next unit.
+__device__ __forceinline__ void next_unit(const AttnParams& P, Place& at) {
+    at.t = 0;
+    if (++at.rt < P.rt_count) return;
+    at.rt = 0;
+    if (++at.h < P.cache.heads) return;
+    at.h = 0;
+    at.sp = span_at(P, ++at.s);
 }
 
 template <class F>
@@ -280,27 +274,25 @@ struct Warp {
         lim = F::SPLIT ? 29.0f : 15.0f;
     }
 
-    // Loads the query rows of unit u of sequence s.
-    __device__ __forceinline__ void load_queries(const AttnParams& P, const Place& at, volatile Held& held, int rt_count, int group, int lane) {
+    // Loads the unit's query rows.
+    __device__ __forceinline__ void load_queries(const AttnParams& P, const Place& at, volatile Held& held, int lane) {
         const int g = lane >> 2, c = lane & 3;
-        const int h = at.u / rt_count, rt = at.u - h * rt_count, rows = P.tokens * group;
-        const int first = at.sp.len - at.sp.nl;
-        const int last_row = min((rt + 1) * F::RC, rows) - 1;
-        held.minpos = max(first + rt * F::RC / group, 0);
-        held.maxpos = min(first + last_row / group, at.sp.len - 1);
+        const int row0 = at.rt * F::RC, first = at.sp.len - at.sp.nl;
+        held.minpos = max(first + token_of(P, row0), 0);
+        held.maxpos = min(first + token_of(P, min(row0 + F::RC, P.rows) - 1), at.sp.len - 1);
 #pragma unroll
         for (int nt = 0; nt < F::NT; ++nt) {
             // column g of the tile: a row, or one of its two parts
-            const int row = rt * F::RC + nt * F::RPL * 4 + (F::SPLIT ? g >> 1 : g);
+            const int row = row0 + nt * F::RPL * 4 + (F::SPLIT ? g >> 1 : g);
             float v[F::NB][8], top = 0.0f;
-            if (row < rows) {
-                const RowAt r = row_of(P, at.sp, h, group, row);
+            if (row < P.rows) {
+                const RowAt r = row_of(P, at.sp.len, at.sp.nl, at.h, row);
                 const int64_t base = row_at(P.q, at.s, r.i, r.hq);
 #pragma unroll
                 for (int b = 0; b < F::NB; ++b) {
                     float lo[4], hi[4];
-                    load4(P.q, base + 32 * b + 4 * c, lo);
-                    load4(P.q, base + 32 * b + 16 + 4 * c, hi);
+                    load_four<F::T>(P.q, base + 32 * b + 4 * c, lo);
+                    load_four<F::T>(P.q, base + 32 * b + 16 + 4 * c, hi);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         v[b][j] = lo[j], v[b][4 + j] = hi[j];
@@ -365,7 +357,7 @@ struct Warp {
                 const float fr = __shfl_sync(kFull, fg, 8 * c + 4 * r);
                 f[nt][r] = F::MOD ? kLog2e : fmaxf(fr * kLog2e, 0x1p-140f);  // not 0: -inf is to stay that
                 if (F::MOD) {
-                    const RowAt ra = row_of(P, at.sp, h, group, min(rt * F::RC + (nt * 4 + c) * F::RPL + r, rows - 1));
+                    const RowAt ra = row_of(P, at.sp.len, at.sp.nl, at.h, min(row0 + (nt * 4 + c) * F::RPL + r, P.rows - 1));
                     pos[nt][r] = first + ra.i;
                     scale[nt][r] = fr, slope[nt][r] = P.alibi ? P.alibi[ra.hq] : 0.0f;
                 }
@@ -590,13 +582,12 @@ struct Warp {
     __device__ __forceinline__ void mask(const AttnParams& P, const volatile Held& held, int p0, int lane, float (&s)[2][F::NT][F::VPT]) {
         const int g = lane >> 2, c = lane & 3;
         const int window = P.window > 0 ? P.window : kNoWindow;
-        const int group = P.q_heads / P.cache.heads, rows = P.tokens * group, rt_count = (rows + F::RC - 1) / F::RC;
-        const int row0 = held.at.u % rt_count * F::RC + c * F::RPL, first = held.at.sp.len - held.at.sp.nl;
+        const int row0 = held.at.rt * F::RC + c * F::RPL, first = held.at.sp.len - held.at.sp.nl;
 #pragma unroll
         for (int nt = 0; nt < F::NT; ++nt)
 #pragma unroll
             for (int r = 0; r < F::RPL; ++r) {
-                const int at = first + min(row0 + nt * F::RPL * 4 + r, rows - 1) / group;
+                const int at = first + token_of(P, min(row0 + nt * F::RPL * 4 + r, P.rows - 1));
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -688,28 +679,26 @@ struct Producer {
         entry = i < P.seqs.table_pages ? P.seqs.table[s * P.seqs.table_stride + i] : -1;
     }
     // From record r of a page on; `unit` of the unit's records are left.
-    __device__ __forceinline__ void open(const AttnParams& P, volatile Held& held, const Place& at, int rt_count, int page, int base, int r, int unit, int lane) {
-        const int rpp = P.cache.page_size / kGroup;
+    __device__ __forceinline__ void open(const AttnParams& P, volatile Held& held, const Place& at, int page, int base, int r, int unit, int lane) {
         const int pg = __shfl_sync(kFull, entry, page - base);
         good = (uint32_t)pg < (uint32_t)P.cache.pages && !nothing(at.sp);
         if (!good && !nothing(at.sp) && lane == 0) atomicOr(P.ws, kBadPage);
-        const int h = rt_count == 1 ? at.u : at.u / rt_count;
-        from = P.cache.data + (((int64_t)pg * P.cache.heads + h) * rpp + r) * F::REC;
-        run = min(rpp - r, unit);
+        from = P.cache.data + (((int64_t)pg * P.cache.heads + at.h) * P.rpp + r) * F::REC;
+        run = min(P.rpp - r, unit);
         held.page = page, held.base = base, held.unit_left = unit - run;
     }
-    __device__ __forceinline__ void seek(const AttnParams& P, volatile Held& held, const Place& at, int rt_count, int lane) {
-        const int rpp = P.cache.page_size / kGroup, tile = at.sp.tile0 + at.t, page = tile / rpp;
+    __device__ __forceinline__ void seek(const AttnParams& P, volatile Held& held, const Place& at, int lane) {
+        const int tile = at.sp.tile0 + at.t, page = (int)((uint32_t)tile / (uint32_t)P.rpp);
         put(held.next, at);
         load_entries(P, at.s, page, lane);
-        open(P, held, at, rt_count, page, page, tile - page * rpp, at.sp.n - at.t, lane);
+        open(P, held, at, page, page, tile - page * P.rpp, at.sp.n - at.t, lane);
     }
-    __device__ __forceinline__ void start(const AttnParams& P, volatile Held& held, const Place& place, int tiles, int rt_count, int lane) {
+    __device__ __forceinline__ void start(const AttnParams& P, volatile Held& held, const Place& place, int tiles, int lane) {
         left = tiles;
         filled = 0;
-        seek(P, held, place, rt_count, lane);
+        seek(P, held, place, lane);
     }
-    __device__ __forceinline__ void issue(const AttnParams& P, volatile Held& held, int units, int rt_count, uint8_t* slot, uint64_t* bar, uint32_t bit, int lane) {
+    __device__ __forceinline__ void issue(const AttnParams& P, volatile Held& held, uint8_t* slot, uint64_t* bar, uint32_t bit, int lane) {
         if (left == 0) return;
         if (good) filled |= bit;
         if (good && lane == 0) {
@@ -725,23 +714,19 @@ struct Producer {
                 const int page = held.page + 1;
                 int base = held.base;
                 if (page - base == 32) load_entries(P, at.s, base = page, lane);
-                open(P, held, at, rt_count, page, base, 0, unit, lane);
+                open(P, held, at, page, base, 0, unit, lane);
             } else {
-                at.t = 0;
-                if (++at.u == units) {
-                    at.u = 0;
-                    at.sp = span_at(P, ++at.s);
-                }
-                seek(P, held, at, rt_count, lane);
+                next_unit(P, at);
+                seek(P, held, at, lane);
             }
         }
     }
 };
 
 // DIM sums of a row over the lanes of a warp: lane's elements 4 lane .. or 2 lane ..
-template <int DIM>
+template <class F>
 struct RowSum {
-    static constexpr int V = DIM == 64 ? 2 : 4, N = DIM / 32 / V;
+    static constexpr int DIM = F::DIM, V = DIM == 64 ? 2 : 4, N = DIM / 32 / V;
     float v[N][V];
     __device__ __forceinline__ RowSum() {
 #pragma unroll
@@ -795,16 +780,14 @@ struct RowSum {
         }
     }
     __device__ __forceinline__ void write(const AttnParams& P, int s, const RowAt& r, float m, float l, int lane) const {
-        const RowOut to = row_out(P, s, r, l);
+        const int64_t to = row_at(P.out, s, r.i, r.hq);
+        const float inv = inverse(r, l);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int64_t at = to.at + element(i, lane);
-            if constexpr (V == 4) {
-                const float t[4] = {result(v[i][0], to.inv), result(v[i][1], to.inv), result(v[i][2], to.inv), result(v[i][3], to.inv)};
-                store4(P.out, at, t);
-            } else {
-                store2(P.out, at, result(v[i][0], to.inv), result(v[i][1], to.inv));
-            }
+            float t[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) t[j] = result(v[i][j], inv);
+            store_some<F::T>(P.out, to + element(i, lane), t);
         }
         if (lane == 0) write_lse(P, s, r, m, l);
     }
@@ -824,83 +807,71 @@ __device__ __forceinline__ float warp_sum(float v) {
 template <class F>
 __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __grid_constant__ AttnParams P) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t cut_start[2];  // units that this CTA shares with others: its first, its last
-    __shared__ int cut_entry[2], joins[2];
+    __shared__ int cut_entry[2], joins[2];  // units that this CTA shares with others: its first, its last
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float* const parts = reinterpret_cast<float*>(smem + F::OFF_PART);
     float* const ml = reinterpret_cast<float*>(smem + F::OFF_ML);  // [warp][first, last][ref, l][RC]
     Entry* const ents = reinterpret_cast<Entry*>(smem + F::OFF_ENT);
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + F::OFF_BAR) + warp * F::STAGES;
-    int64_t* const pre = reinterpret_cast<int64_t*>(smem + F::OFF_PRE);
+    int* const pre = reinterpret_cast<int*>(smem + F::OFF_PRE);
     uint8_t* const ring = smem + warp * F::RING;
     volatile Held& held = reinterpret_cast<Held*>(smem + F::OFF_HELD)[warp];
-
-    const int group = P.q_heads / P.cache.heads;
-    const int rows = P.tokens * group, rt_count = (rows + F::RC - 1) / F::RC;
-    const int units = P.cache.heads * rt_count;
-
-    if (lane == 0) {
-        for (int i = 0; i < F::STAGES; ++i) q4dev::mbar_init(bars + i, 1);
-        q4dev::mbar_fence_init();
-        ents[2 * warp].part = ents[2 * warp + 1].part = -1;
-    }
-    if (tid < 2) cut_entry[tid] = -1;
 
     // tiles of one unit of all sequences, and of those before each run of `run` sequences
     // (up to 32 sequences: every warp for itself, a lane a sequence)
     const bool few = P.seqs.count <= 32;
     const int run = few ? 1 : (P.seqs.count + F::THREADS - 1) / F::THREADS;
     Span mine = {0, 0, 0, 0};
-    int64_t all, before = 0;  // few: tiles before the lane's sequence
-    if (few) {
-        if (lane < P.seqs.count) mine = span_at(P, lane);
-        int64_t inc = mine.n;
+    if (few && lane < P.seqs.count) mine = span_at(P, lane);
+    if (lane == 0) {
+        for (int i = 0; i < F::STAGES; ++i) q4dev::mbar_init(bars + i, 1);
+        q4dev::mbar_fence_init();
+        ents[2 * warp].part = ents[2 * warp + 1].part = -1;
+    }
+    if (tid < 2) cut_entry[tid] = -1;
+    int all, before = 0;  // few: tiles before the lane's sequence
+    {
+        int sum = mine.n;
+        if (!few)
+            for (int i = 0, s = tid * run; i < run && s < P.seqs.count; ++i, ++s) sum += span_at(P, s).n;
+        int inc = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(kFull, inc, off);
+            const int o = __shfl_up_sync(kFull, inc, off);
             if (lane >= off) inc += o;
         }
         all = __shfl_sync(kFull, inc, 31);
-        before = inc - mine.n;
-        __syncwarp();
-    } else {
-        const int64_t s0 = (int64_t)tid * run;
-        int64_t sum = 0;
-        for (int i = 0; i < run && s0 + i < P.seqs.count; ++i) sum += span_at(P, (int)s0 + i).n;
-        int64_t inc = sum;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(kFull, inc, off);
-            if (lane >= off) inc += o;
-        }
-        if (lane == 31) pre[F::THREADS + warp] = inc;
+        before = inc - sum;
+    }
+    if (!few) {
+        if (lane == 31) pre[F::THREADS + warp] = all;
         __syncthreads();
-        int64_t lower = 0;
+        int lower = 0;
         all = 0;
 #pragma unroll
         for (int w = 0; w < F::WARPS; ++w) {
-            const int64_t o = pre[F::THREADS + w];
+            const int o = pre[F::THREADS + w];
             lower += w < warp ? o : 0;
             all += o;
         }
-        pre[tid] = lower + inc - sum;
+        pre[tid] = lower + before;
         __syncthreads();
     }
-    const int64_t total = all * units;
-    const int ctas = ctas_of(total, units, P.seqs.count, F::WARPS, gridDim.x);
+    const int total = all * P.units;
+    const int ctas = ctas_of(total, P.units, P.seqs.count, F::WARPS, gridDim.x);
     if ((int)blockIdx.x >= ctas) return;
     const Parts cp(total, ctas);
-    const int64_t a = cp.begin(blockIdx.x), z = cp.begin(blockIdx.x + 1);
+    const int a = cp.begin(blockIdx.x), z = cp.begin(blockIdx.x + 1);
     const Parts wp(z - a, F::WARPS);
-    const int64_t wa = a + wp.begin(warp);
-    int todo = (int)wp.begin(warp + 1) - (int)wp.begin(warp);
+    const int wa = a + wp.begin(warp);
+    int todo = wp.q + (warp < wp.r);
 
     if (todo > 0) {
         // the place of tile wa
         {
             Place at;
-            const int64_t y = units == 1 ? wa : quotient(wa, units);
-            int64_t rest;
+            const int y = (int)((uint32_t)wa / (uint32_t)P.units);
+            int rest;
             if (few) {
                 at.s = 31 - __clz(__ballot_sync(kFull, before <= y && lane < P.seqs.count));
                 rest = y - __shfl_sync(kFull, before, at.s);
@@ -912,7 +883,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                 int lo = 0, hi = F::THREADS;  // pre[lo] <= y < pre[hi]
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) / 2;
-                    if (pre[mid] <= y && (int64_t)mid * run < P.seqs.count)
+                    if (pre[mid] <= y && mid * run < P.seqs.count)
                         lo = mid;
                     else
                         hi = mid;
@@ -925,16 +896,18 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                     at.sp = span_at(P, ++at.s);
                 }
             }
-            const int64_t off = wa - (y - rest) * units;
-            at.u = units == 1 ? 0 : (int)quotient(off, at.sp.n);
-            at.t = (int)(off - (int64_t)at.u * at.sp.n);
+            const int off = wa - (y - rest) * P.units, u = (int)((uint32_t)off / (uint32_t)at.sp.n);
+            at.t = off - u * at.sp.n;
+            at.h = u, at.rt = 0;
+            if (P.rt_count > 1) at.h = (int)((uint32_t)u / (uint32_t)P.rt_count), at.rt = u - at.h * P.rt_count;
             held.start = wa - at.t;
             put(held.at, at);
         }
+        __syncwarp();  // the barriers
         Producer<F> prod;
-        prod.start(P, held, get(held.at), todo, rt_count, lane);
+        prod.start(P, held, get(held.at), todo, lane);
 #pragma unroll
-        for (int i = 0; i < F::STAGES; ++i) prod.issue(P, held, units, rt_count, ring + i * F::REC, bars + i, 1u << i, lane);
+        for (int i = 0; i < F::STAGES; ++i) prod.issue(P, held, ring + i * F::REC, bars + i, 1u << i, lane);
 
         Warp<F> w;
         uint32_t used = 0, phases = 0;  // tiles done; bit i: parity of the next wait on stage i
@@ -946,7 +919,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                 n = min(at.sp.n - at.t, todo);
                 p0 = (at.sp.tile0 + at.t) * kGroup;
                 if (!nothing(at.sp)) {
-                    w.load_queries(P, at, held, rt_count, group, lane);
+                    w.load_queries(P, at, held, lane);
                     w.start();
                 }
             }
@@ -965,30 +938,33 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                 }
                 __syncwarp();
                 prod.filled >>= 1;
-                prod.issue(P, held, units, rt_count, slot, bars + stage, 1u << (F::STAGES - 1), lane);
+                prod.issue(P, held, slot, bars + stage, 1u << (F::STAGES - 1), lane);
                 ++used;
                 p0 += kGroup;
             }
             Place at = get(held.at);
-            const bool whole = n == at.sp.n, empty = nothing(at.sp);
+            const bool whole = n == at.sp.n;
             todo -= n;
-            const int h = rt_count == 1 ? at.u : at.u / rt_count, row0 = (at.u - h * rt_count) * F::RC;
-            if (empty) {
-                for (int row = row0; row < min(row0 + F::RC, rows); ++row)
-                    RowSum<F::DIM>().write(P, at.s, row_of(P, at.sp, h, group, row), -INFINITY, 0.0f, lane);
+            const int row0 = at.rt * F::RC;
+            if (nothing(at.sp)) {
+                for (int row = row0; row < min(row0 + F::RC, P.rows); ++row)
+                    RowSum<F>().write(P, at.s, row_of(P, at.sp.len, at.sp.nl, at.h, row), 0.0f, 0.0f, lane);
             } else if (whole) {
+                struct To {
+                    int64_t at;
+                    float inv;
+                };
                 w.finish(
                     lane,
                     [&](int row, float m, float l) {
-                        const bool there = row0 + row < rows;
-                        const RowAt r = row_of(P, at.sp, h, group, there ? row0 + row : 0);
-                        RowOut to = row_out(P, at.s, r, l);
+                        const bool there = row0 + row < P.rows;
+                        const RowAt r = row_of(P, at.sp.len, at.sp.nl, at.h, there ? row0 + row : 0);
                         if (there && lane < 4) write_lse(P, at.s, r, m, l);
-                        if (!there) to.at = -1;
-                        return to;
+                        return To{there ? row_at(P.out, at.s, r.i, r.hq) : -1, inverse(r, l)};
                     },
-                    [&](const RowOut& to, int x, float v0, float v1) {
-                        if (to.at >= 0) store2(P.out, to.at + x, result(v0, to.inv), result(v1, to.inv));
+                    [&](const To& to, int x, float v0, float v1) {
+                        const float t[2] = {result(v0, to.inv), result(v1, to.inv)};
+                        if (to.at >= 0) store_some<F::T>(P.out, to.at + x, t);
                     });
             } else {
                 // the ring is free once the warp's last tile is done
@@ -1004,17 +980,14 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                     [&](float* to, int x, float v0, float v1) { *reinterpret_cast<float2*>(to + x) = make_float2(v0, v1); });
                 if (lane == 0) {
                     Entry& e = ents[2 * warp + last];
-                    e.start = held.start, e.s = at.s, e.u = at.u, e.n = at.sp.n;
+                    e.start = held.start, e.n = at.sp.n, e.s = at.s, e.h = at.h, e.row0 = row0;
+                    e.len = at.sp.len, e.nl = at.sp.nl;
                     e.part = (int)(p - reinterpret_cast<float*>(smem));
                 }
             }
             if (todo > 0) {
                 held.start = held.start + at.sp.n;
-                at.t = 0;
-                if (++at.u == units) {
-                    at.u = 0;
-                    at.sp = span_at(P, ++at.s);
-                }
+                next_unit(P, at);
                 put(held.at, at);
             }
         }
@@ -1026,10 +999,10 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
     // weights and then the elements
     {
         const bool valid = lane < 2 * F::WARPS && ents[lane].part >= 0;
-        const int64_t mine_start = valid ? ents[lane].start : -1;
+        const int mine_start = valid ? ents[lane].start : -1;
         const int mine_part = valid ? ents[lane].part : 0;
         uint32_t rest = __ballot_sync(kFull, valid);
-        int task = 0;
+        int task = warp;
         while (rest) {
             const int e0 = __ffs(rest) - 1;
             const Entry en = ents[e0];
@@ -1037,40 +1010,42 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
             rest &= ~run_mask;
             const bool whole = en.start >= a && en.start + en.n <= z;
             const int slot = en.start > a;
-            if (!whole && tid == 0) cut_start[slot] = en.start, cut_entry[slot] = e0;
-            const int h = rt_count == 1 ? en.u : en.u / rt_count, row0 = (en.u - h * rt_count) * F::RC;
-            const int n = min(F::RC, rows - row0);
-            for (int row = 0; row < n; ++row) {
-                if (task++ % F::WARPS != warp) continue;
-                const bool in = run_mask >> lane & 1;
+            if (!whole && tid == 0) cut_entry[slot] = e0;
+            const int n = min(F::RC, P.rows - en.row0);
+            const bool in = run_mask >> lane & 1;
+            for (; task < n; task += F::WARPS) {
+                const int row = task;
                 const float m = in ? ml[lane * 2 * F::RC + row] : kNoRef;
+                float l = in ? ml[lane * 2 * F::RC + F::RC + row] : 0.0f;
                 const float top = warp_max(m);
                 const float k = in ? weight(m, top) : 0.0f;
-                const float l = warp_sum(in ? k * ml[lane * 2 * F::RC + F::RC + row] : 0.0f);
-                RowSum<F::DIM> sum;
+                l = warp_sum(in ? k * l : 0.0f);
+                RowSum<F> sum;
+#pragma unroll 4
                 for (uint32_t left = run_mask; left; left &= left - 1) {
                     const int e = __ffs(left) - 1;
                     sum.template add<false>(reinterpret_cast<const float*>(smem) + __shfl_sync(kFull, mine_part, e) + row * F::ROW,
                                             __shfl_sync(kFull, k, e), lane);
                 }
                 if (whole) {
-                    const Span sp = span_at(P, en.s);
-                    sum.write(P, en.s, row_of(P, sp, h, group, row0 + row), top, l, lane);
+                    sum.write(P, en.s, row_of(P, en.len, en.nl, en.h, en.row0 + row), top, l, lane);
                 } else {
-                    float* const to = P.parts + ((int64_t)blockIdx.x * 2 + slot) * F::WPART;
+                    float* const to = P.parts + (blockIdx.x * 2 + slot) * F::WPART;
                     sum.keep(to + row * F::DIM, lane);
                     if (lane == 0) to[F::RC * F::DIM + row] = top, to[F::RC * F::DIM + F::RC + row] = l;
                 }
             }
+            task -= n;  // the next unit's rows go on with the next warp
         }
     }
     __syncthreads();
+    if (cut_entry[0] < 0 && cut_entry[1] < 0) return;
     // and those that CTAs cut: the last to arrive joins them in order
     if (tid < 2) {
         int join = 0;
         if (cut_entry[tid] >= 0) {
-            const int64_t start = cut_start[tid];
-            const int i0 = cp.of(start), i1 = cp.of(start + ents[cut_entry[tid]].n - 1);
+            const Entry& en = ents[cut_entry[tid]];
+            const int i0 = cp.of(en.start), i1 = cp.of(en.start + en.n - 1);
             const int sh = 8 * (i0 & 3);
             uint32_t* const ticket = P.ws + 1 + (i0 >> 2);
             __threadfence();
@@ -1084,52 +1059,58 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
         joins[tid] = join;
     }
     __syncthreads();
+#pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         if (!joins[k]) continue;
         const Entry en = ents[cut_entry[k]];
         const int i0 = cp.of(en.start), i1 = cp.of(en.start + en.n - 1);
-        const int slot0 = en.start > cp.begin(i0);
-        const int h = rt_count == 1 ? en.u : en.u / rt_count, row0 = (en.u - h * rt_count) * F::RC;
-        const Span sp = span_at(P, en.s);
-        auto part = [&](int cta) { return P.parts + ((int64_t)cta * 2 + (cta == i0 ? slot0 : 0)) * F::WPART; };
+        const float* const part0 = P.parts + (i0 * 2 + (en.start > cp.begin(i0))) * F::WPART;  // the other CTAs': in their first slot
+        auto part = [&](int i) { return i == 0 ? part0 : P.parts + (i0 + i) * 2 * F::WPART; };
         // chunks of parts by warp, all loads of one in flight at once; the chunks' sums meet in
         // the rings' memory
-        const int n = i1 - i0 + 1, nrows = min(F::RC, rows - row0);
-        const int chunks = n <= 8 * kJoin ? (n + 7) / 8 : (n + 15) / 16;
+        const int n = i1 - i0 + 1, nrows = min(F::RC, P.rows - en.row0);
         const int per = n <= 8 * kJoin ? 8 : 16;
-        float* const sums = reinterpret_cast<float*>(smem);  // [row][chunk][ref, l][DIM]: no more than kJoin chunks
-        __syncthreads();
-        for (int task = warp; task < nrows * chunks; task += F::WARPS) {
-            const int row = task / chunks, c0 = (task - row * chunks) * per, m = min(per, n - c0);
-            RowSum<F::DIM> sum;
-            float ref = kNoRef, l = 0.0f;
-            if (lane < m) {
-                const float* const q = part(i0 + c0 + lane) + F::RC * F::DIM + row;
-                ref = __ldcg(q), l = __ldcg(q + F::RC);
+        const int chunks = (n + per - 1) / per;
+        float* const sums = reinterpret_cast<float*>(smem);  // [chunk][row][DIM sums, ref, l]
+        if (k == 1 && joins[0]) __syncthreads();
+        for (int task = warp, chunk = 0; chunk < chunks; task -= nrows, ++chunk)
+            for (; task < nrows; task += F::WARPS) {
+                const int row = task, c0 = chunk * per, m = min(per, n - c0);
+                float ref = kNoRef, l = 0.0f;
+                if (lane < m) {
+                    const float* const q = part(c0 + lane) + F::RC * F::DIM + row;
+                    ref = __ldcg(q), l = __ldcg(q + F::RC);
+                }
+                RowSum<F> sum, v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < m) v[i].load(part(c0 + i) + row * F::DIM, lane);
+                const float top = warp_max(ref);
+                const float w = lane < m ? weight(ref, top) : 0.0f;
+                l = warp_sum(l * w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum.add(v[i], __shfl_sync(kFull, w, i));
+                for (int i = 8; i < m; ++i) sum.template add<true>(part(c0 + i) + row * F::DIM, __shfl_sync(kFull, w, i), lane);
+                if (chunks == 1) {
+                    sum.write(P, en.s, row_of(P, en.len, en.nl, en.h, en.row0 + row), top, l, lane);
+                } else {
+                    float* const to = sums + (chunk * nrows + row) * (F::DIM + 4);
+                    sum.keep(to, lane);
+                    if (lane == 0) to[F::DIM] = top, to[F::DIM + 1] = l;
+                }
             }
-            RowSum<F::DIM> v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < m) v[i].load(part(i0 + c0 + i) + row * F::DIM, lane);
-            const float top = warp_max(ref);
-            const float k = lane < m ? weight(ref, top) : 0.0f;
-            l = warp_sum(l * k);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum.add(v[i], __shfl_sync(kFull, k, i));
-            for (int i = 8; i < m; ++i) sum.template add<true>(part(i0 + c0 + i) + row * F::DIM, __shfl_sync(kFull, k, i), lane);
-            float* const to = sums + task * (F::DIM + 4);
-            sum.keep(to, lane);
-            if (lane == 0) to[F::DIM] = top, to[F::DIM + 1] = l;
-        }
+        if (chunks == 1) continue;
         __syncthreads();
         for (int row = warp; row < nrows; row += F::WARPS) {
-            const float* const from = sums + row * chunks * (F::DIM + 4);
-            const float ref = lane < chunks ? from[lane * (F::DIM + 4) + F::DIM] : kNoRef;
-            const float top = warp_max(ref), k = lane < chunks ? weight(ref, top) : 0.0f;
-            const float l = warp_sum(lane < chunks ? k * from[lane * (F::DIM + 4) + F::DIM + 1] : 0.0f);
-            RowSum<F::DIM> sum;
-            for (int i = 0; i < chunks; ++i) sum.template add<false>(from + i * (F::DIM + 4), __shfl_sync(kFull, k, i), lane);
-            sum.write(P, en.s, row_of(P, sp, h, group, row0 + row), top, l, lane);
+            const float* const from = sums + row * (F::DIM + 4);
+            const int stride = nrows * (F::DIM + 4);
+            const float ref = lane < chunks ? from[lane * stride + F::DIM] : kNoRef;
+            float l = lane < chunks ? from[lane * stride + F::DIM + 1] : 0.0f;
+            const float top = warp_max(ref), w = lane < chunks ? weight(ref, top) : 0.0f;
+            l = warp_sum(w * l);
+            RowSum<F> sum;
+            for (int i = 0; i < chunks; ++i) sum.template add<false>(from + i * stride, __shfl_sync(kFull, w, i), lane);
+            sum.write(P, en.s, row_of(P, en.len, en.nl, en.h, en.row0 + row), top, l, lane);
         }
     }
 }
@@ -1140,50 +1121,59 @@ cudaError_t setup() {
 }
 
 template <class F>
-cudaError_t run(const AttnParams& P, int num_sms, cudaStream_t stream) {
+cudaError_t run(AttnParams P, int num_sms, cudaStream_t stream) {
+    P.rt_count = (P.rows + F::RC - 1) / F::RC;
+    P.units = P.cache.heads * P.rt_count;
     const int grid = num_sms < kMaxCtas ? num_sms : kMaxCtas;
     kv_attention_kernel<F><<<grid, F::THREADS, F::SMEM, stream>>>(P);
     return cudaGetLastError();
 }
 
-// Calls fn with the configuration of a call: the row tile that holds the unit's rows, if
-// one does, and the arithmetic that the types and the scores ask for.
-template <int DIM, class Fn>
-cudaError_t with_dim(bool split, bool mod, int rows, Fn fn) {
-    const bool one = DIM == 256 || rows <= (split ? 4 : 8);
+// Calls fn with the configuration of a call: the types, and the smaller row tile where it
+// holds all rows.
+template <int DIM, int T, class Fn>
+cudaError_t with_type(bool mod, int rows, Fn fn) {
     constexpr int WIDE = DIM == 256 ? 1 : 2;
-    if (split) {
-        if (mod) return one ? fn(Cfg<DIM, 1, true, true>()) : fn(Cfg<DIM, WIDE, true, true>());
-        return one ? fn(Cfg<DIM, 1, true, false>()) : fn(Cfg<DIM, WIDE, true, false>());
-    }
-    if (mod) return one ? fn(Cfg<DIM, 1, false, true>()) : fn(Cfg<DIM, WIDE, false, true>());
-    return one ? fn(Cfg<DIM, 1, false, false>()) : fn(Cfg<DIM, WIDE, false, false>());
+    if (DIM == 256 || rows <= Cfg<DIM, 1, T, false>::RC) return mod ? fn(Cfg<DIM, 1, T, true>()) : fn(Cfg<DIM, 1, T, false>());
+    return mod ? fn(Cfg<DIM, WIDE, T, true>()) : fn(Cfg<DIM, WIDE, T, false>());
+}
+template <int DIM, class Fn>
+cudaError_t with_dim(int type, bool mod, int rows, Fn fn) {
+    return type == Q4_BF16   ? with_type<DIM, Q4_BF16>(mod, rows, fn)
+           : type == Q4_F32  ? with_type<DIM, Q4_F32>(mod, rows, fn)
+           : type == Q4_F16  ? with_type<DIM, Q4_F16>(mod, rows, fn)
+           : type == kAnyBf16 ? with_type<DIM, kAnyBf16>(mod, rows, fn)
+                             : with_type<DIM, kAnyRows>(mod, rows, fn);
 }
 
 }  // namespace
 
+template <int DIM>
 cudaError_t setup_kv_attention() {
-    for (int i = 0; i < 8; ++i) {
-        auto fn = [](auto f) { return setup<decltype(f)>(); };
-        const int rows = i & 4 ? 64 : 1;
-        cudaError_t e = with_dim<64>(i & 1, i & 2, rows, fn);
-        if (e == cudaSuccess) e = with_dim<128>(i & 1, i & 2, rows, fn);
-        if (e == cudaSuccess) e = with_dim<256>(i & 1, i & 2, rows, fn);
-        if (e != cudaSuccess) return e;
-    }
+    for (int type : {(int)Q4_F32, (int)Q4_F16, (int)Q4_BF16, kAnyRows, kAnyBf16})
+        for (int i = 0; i < 4; ++i) {
+            const cudaError_t e = with_dim<DIM>(type, i & 1, i & 2 ? 64 : 1, [](auto f) { return setup<decltype(f)>(); });
+            if (e != cudaSuccess) return e;
+        }
     return cudaSuccess;
 }
 
-// Floats of the partial results of any call with this head dimension: two a CTA, 16 rows.
-size_t kv_attention_part_floats(int dim) { return (size_t)kMaxCtas * 2 * (dim == 256 ? 8 : 16) * (dim + 2); }
-
-cudaError_t launch_kv_attention(int dim, const AttnParams& P, int num_sms, cudaStream_t stream) {
-    const bool split = P.q.type != Q4_BF16 || P.out.type != Q4_BF16, mod = P.softcap > 0.0f || P.alibi;
-    const int rows = P.tokens * (P.q_heads / P.cache.heads);
-    auto fn = [&](auto f) { return run<decltype(f)>(P, num_sms, stream); };
-    if (dim == 64) return with_dim<64>(split, mod, rows, fn);
-    if (dim == 128) return with_dim<128>(split, mod, rows, fn);
-    return with_dim<256>(split, mod, rows, fn);
+template <int DIM>
+cudaError_t launch_kv_attention(const AttnParams& P, int num_sms, cudaStream_t stream) {
+    const bool vec = P.q.vec && P.out.vec, same = P.q.type == P.out.type;
+    const int type = !same ? kAnyRows : vec ? P.q.type : P.q.type == Q4_BF16 ? kAnyBf16 : kAnyRows;
+    return with_dim<DIM>(type, P.softcap > 0.0f || P.alibi, P.rows, [&](auto f) { return run<decltype(f)>(P, num_sms, stream); });
 }
+
+// Floats of the partial results of any call: two a CTA, of the widest row tile.
+template <int DIM>
+size_t kv_attention_part_floats() {
+    return (size_t)kMaxCtas * 2 * Cfg<DIM, DIM == 256 ? 1 : 2, Q4_BF16, false>::WPART;
+}
+
+#define Q4KV_ATTENTION(DIM)                                                                       \
+    template cudaError_t setup_kv_attention<DIM>();                                               \
+    template cudaError_t launch_kv_attention<DIM>(const AttnParams&, int, cudaStream_t);          \
+    template size_t kv_attention_part_floats<DIM>();
 
 }  // namespace q4kv

@@ -1,0 +1,6 @@
+// Attention over the 4-bit cache for a head dimension of 64.
+#include "q4_kv_attn.cuh"
+
+namespace q4kv {
+Q4KV_ATTENTION(64)
+}  // namespace q4kv

@@ -9,7 +9,11 @@
 
 namespace q4kv {
 cudaError_t launch_kv_move(bool write, int dim, const MoveParams& P, cudaStream_t stream);
+// One of these for each head dimension.
+template <int DIM>
 cudaError_t setup_kv_attention();
-size_t kv_attention_part_floats(int dim);
-cudaError_t launch_kv_attention(int dim, const AttnParams& P, int num_sms, cudaStream_t stream);
+template <int DIM>
+cudaError_t launch_kv_attention(const AttnParams& P, int num_sms, cudaStream_t stream);
+template <int DIM>
+size_t kv_attention_part_floats();
 }  // namespace q4kv

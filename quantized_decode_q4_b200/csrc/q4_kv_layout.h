@@ -99,6 +99,10 @@ struct AttnParams {
     float* parts;
     float scale, softcap;
     int32_t tokens, q_heads, window;
+    int32_t group, rows;   // query heads of a key/value head; times tokens
+    uint32_t group_inv;    // ceil(2^32 / group), 0 for a group of 1
+    int32_t rpp;           // records of a page
+    int32_t rt_count, units;  // row tiles of a key/value head, units of a sequence: set at the launch
 };
 
 }  // namespace q4kv

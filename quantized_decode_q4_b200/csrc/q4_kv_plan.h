@@ -40,32 +40,26 @@ __host__ __device__ __forceinline__ Span span_of(int len, int nl, int tokens, in
 
 __host__ __device__ __forceinline__ bool nothing(const Span& s) { return s.len <= 0 || s.nl <= 0; }
 
-// x / d, in 32 bits where both fit (a 64-bit division costs some hundred cycles).
-__host__ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t d) {
-    return ((uint64_t)x | (uint64_t)d) >> 32 ? x / d : (int64_t)((uint32_t)x / (uint32_t)d);
-}
-
 // CTAs that get work. Each warp should have at least one tile; a sequence alone whose units
 // are short takes one CTA a unit, since up to three more tiles a warp cost less than
-// joining a unit's parts through memory.
-__host__ __device__ __forceinline__ int ctas_of(int64_t total, int units, int count, int warps, int grid) {
-    if (count == 1 && units <= grid && total <= (int64_t)units * 4 * warps) return units;
-    const int64_t want = quotient(total + warps - 1, warps);
-    return want < grid ? (int)want : grid;
+// joining a unit's parts through memory. (The host refuses calls whose tables could hold 2^31 tiles.)
+__host__ __device__ __forceinline__ int ctas_of(int total, int units, int count, int warps, int grid) {
+    if (count == 1 && units <= grid && total <= units * 4 * warps) return units;
+    const int want = (int)(((uint32_t)total + warps - 1) / (uint32_t)warps);
+    return want < grid ? want : grid;
 }
 
 // `total` tiles in `parts` contiguous ranges that differ by one at most.
 struct Parts {
-    int64_t q;
-    int32_t r;
-    __host__ __device__ __forceinline__ Parts(int64_t total, int parts) {
-        q = quotient(total, parts);
-        r = (int32_t)(total - q * parts);
+    int q, r;
+    __host__ __device__ __forceinline__ Parts(int total, int parts) {
+        q = (int)((uint32_t)total / (uint32_t)parts);
+        r = total - q * parts;
     }
-    __host__ __device__ __forceinline__ int64_t begin(int i) const { return i * q + (i < r ? i : r); }
-    __host__ __device__ __forceinline__ int of(int64_t x) const {  // the range that holds tile x
-        const int64_t longer = r * (q + 1);
-        return x < longer ? (int)quotient(x, q + 1) : (int)(r + quotient(x - longer, q));
+    __host__ __device__ __forceinline__ int begin(int i) const { return i * q + (i < r ? i : r); }
+    __host__ __device__ __forceinline__ int of(int x) const {  // the range that holds tile x
+        const int longer = r * (q + 1);
+        return x < longer ? (int)((uint32_t)x / (uint32_t)(q + 1)) : r + (int)((uint32_t)(x - longer) / (uint32_t)q);
     }
 };
 
