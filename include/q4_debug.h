@@ -99,6 +99,13 @@ int q4_debug_check_kv_layout(int dim);
 int q4_debug_check_kv_plan(const int32_t* lens, const int32_t* new_lens, int count, int tokens, int window,
                            int table_tokens, int units, int warps, int grid);
 
+/* q4_kv_attention with every record's barrier expecting 16 bytes more than its copy brings:
+ * each wait runs out (20 ms), the kernel records Q4_ERR_TIMEOUT in the workspace and ends;
+ * what it writes to `out` is of no use. */
+q4_status q4_debug_kv_attention_stall(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
+                                      const q4_rows* q, const q4_kv_scores* scores, const q4_rows* out, void* ws,
+                                      size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "../../include/q4.h"
+#include "../../include/q4_debug.h"
 #include "q4_host.h"
 #include "q4_kv_host.h"
 
@@ -94,36 +95,9 @@ q4_status move_call(bool write, const q4_kv_cache* cache, const q4_kv_seqs* seqs
     return Q4_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t q4_kv_cache_bytes(int64_t pages, int32_t heads, int32_t dim, int32_t page_size) {
-    int64_t bytes = 0;
-    return cache_size(pages, heads, dim, page_size, &bytes) == Q4_OK ? (size_t)bytes : 0;
-}
-
-q4_status q4_kv_write(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, const q4_rows* k,
-                      const q4_rows* v, void* stream) {
-    return move_call(true, cache, seqs, nullptr, tokens, k, v, stream);
-}
-
-q4_status q4_kv_read(const q4_kv_cache* cache, const q4_kv_seqs* seqs, const int32_t* starts, int32_t tokens,
-                     const q4_rows* k, const q4_rows* v, void* stream) {
-    return move_call(false, cache, seqs, starts, tokens, k, v, stream);
-}
-
-size_t q4_kv_attention_workspace_bytes(int32_t dim) {
-    const size_t floats = dim == 64    ? q4kv::kv_attention_part_floats<64>()
-                          : dim == 128 ? q4kv::kv_attention_part_floats<128>()
-                          : dim == 256 ? q4kv::kv_attention_part_floats<256>()
-                                       : 0;
-    return floats ? (size_t)kHeaderBytes + 4 * floats : 0;
-}
-
-q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
+q4_status attention_call(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
                           const q4_rows* q, const q4_kv_scores* scores, const q4_rows* out, float* lse,
-                          void* ws, size_t ws_bytes, void* stream) {
+                          void* ws, size_t ws_bytes, void* stream, uint32_t tx_extra) {
     q4_status s = check_cache(cache);
     if (s != Q4_OK) return s;
     if ((s = check_seqs(cache, seqs)) != Q4_OK) return s;
@@ -162,6 +136,7 @@ q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int3
     P.group = q_heads / cache->heads;
     P.rows = tokens * P.group;
     P.group_inv = P.group == 1 ? 0u : (uint32_t)(((UINT64_C(1) << 32) + P.group - 1) / P.group);
+    P.tx_extra = tx_extra;
     P.rpp = cache->page_size / q4kv::kGroup;
     auto* const launch = cache->dim == 64    ? q4kv::launch_kv_attention<64>
                          : cache->dim == 128 ? q4kv::launch_kv_attention<128>
@@ -169,6 +144,45 @@ q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int3
     if (cuda_failed(launch(P, num_sms, static_cast<cudaStream_t>(stream)))) return Q4_ERR_CUDA;
     count_launches(1);
     return Q4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t q4_kv_cache_bytes(int64_t pages, int32_t heads, int32_t dim, int32_t page_size) {
+    int64_t bytes = 0;
+    return cache_size(pages, heads, dim, page_size, &bytes) == Q4_OK ? (size_t)bytes : 0;
+}
+
+q4_status q4_kv_write(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, const q4_rows* k,
+                      const q4_rows* v, void* stream) {
+    return move_call(true, cache, seqs, nullptr, tokens, k, v, stream);
+}
+
+q4_status q4_kv_read(const q4_kv_cache* cache, const q4_kv_seqs* seqs, const int32_t* starts, int32_t tokens,
+                     const q4_rows* k, const q4_rows* v, void* stream) {
+    return move_call(false, cache, seqs, starts, tokens, k, v, stream);
+}
+
+size_t q4_kv_attention_workspace_bytes(int32_t dim) {
+    const size_t floats = dim == 64    ? q4kv::kv_attention_part_floats<64>()
+                          : dim == 128 ? q4kv::kv_attention_part_floats<128>()
+                          : dim == 256 ? q4kv::kv_attention_part_floats<256>()
+                                       : 0;
+    return floats ? (size_t)kHeaderBytes + 4 * floats : 0;
+}
+
+q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
+                          const q4_rows* q, const q4_kv_scores* scores, const q4_rows* out, float* lse,
+                          void* ws, size_t ws_bytes, void* stream) {
+    return attention_call(cache, seqs, tokens, q_heads, q, scores, out, lse, ws, ws_bytes, stream, 0u);
+}
+
+q4_status q4_debug_kv_attention_stall(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
+                                      const q4_rows* q, const q4_kv_scores* scores, const q4_rows* out, void* ws,
+                                      size_t ws_bytes, void* stream) {
+    return attention_call(cache, seqs, tokens, q_heads, q, scores, out, nullptr, ws, ws_bytes, stream, 16u);
 }
 
 }  // extern "C"

@@ -313,19 +313,18 @@ struct Warp {
             float off[F::NB];
 #pragma unroll
             for (int b = 0; b < F::NB; ++b) {
-                float w[8], sum = 0.0f;
+                float sum = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float x = v[b][j] * up;
-                    float y = __half2float(__float2half_rn(x));
-                    if (F::SPLIT && (g & 1)) y = __half2float(__float2half_rn(x - y));
-                    sum += y;
-                    w[j] = F::SPLIT || j < 4 ? y : y * 0.0625f;  // codes in place: the upper 16 are read 16 times too large
+                for (int j = 0; j < 4; ++j) {
+                    // elements (4c, 4c + 2), (16 + 4c, ..), (4c + 1, 4c + 3), (17 + 4c, ..)
+                    const int at = (j & 1) * 4 + j / 2;
+                    const float x = v[b][at] * up, y = v[b][at + 2] * up;
+                    uint32_t h = pack_half2(x, y);
+                    if (F::SPLIT && (g & 1)) h = pack_half2(x - half_lo(h), y - half_hi(h));
+                    if (!F::SPLIT) sum += half_lo(h) + half_hi(h);
+                    // codes in place: the upper 16 are read 16 times too large
+                    qb[nt][b][j] = F::SPLIT || !(j & 1) ? h : mul_half2(h, 0x2c002c00u);  // 1 / 16
                 }
-                qb[nt][b][0] = pack_half2(w[0], w[2]);
-                qb[nt][b][1] = pack_half2(w[4], w[6]);
-                qb[nt][b][2] = pack_half2(w[1], w[3]);
-                qb[nt][b][3] = pack_half2(w[5], w[7]);
                 if (!F::SPLIT) {
                     sum += __shfl_xor_sync(kFull, sum, 1);
                     sum += __shfl_xor_sync(kFull, sum, 2);
@@ -702,7 +701,7 @@ struct Producer {
         if (left == 0) return;
         if (good) filled |= bit;
         if (good && lane == 0) {
-            q4dev::mbar_arrive_expect_tx(bar, F::REC);
+            q4dev::mbar_arrive_expect_tx(bar, F::REC + P.tx_extra);
             q4dev::bulk_g2s(slot, from, F::REC, bar);
         }
         from += F::REC;
@@ -833,6 +832,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
     {
         int sum = mine.n;
         if (!few)
+#pragma unroll 1
             for (int i = 0, s = tid * run; i < run && s < P.seqs.count; ++i, ++s) sum += span_at(P, s).n;
         int inc = sum;
 #pragma unroll
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
         __syncthreads();
         int lower = 0;
         all = 0;
-#pragma unroll
+#pragma unroll 1
         for (int w = 0; w < F::WARPS; ++w) {
             const int o = pre[F::THREADS + w];
             lower += w < warp ? o : 0;
@@ -881,6 +881,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                 at.sp.nl = __shfl_sync(kFull, mine.nl, at.s);
             } else {
                 int lo = 0, hi = F::THREADS;  // pre[lo] <= y < pre[hi]
+#pragma unroll 1
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) / 2;
                     if (pre[mid] <= y && mid * run < P.seqs.count)
@@ -891,6 +892,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                 at.s = lo * run;
                 rest = y - pre[lo];
                 at.sp = span_at(P, at.s);
+#pragma unroll 1
                 while (rest >= at.sp.n) {
                     rest -= at.sp.n;
                     at.sp = span_at(P, ++at.s);
@@ -906,7 +908,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
         __syncwarp();  // the barriers
         Producer<F> prod;
         prod.start(P, held, get(held.at), todo, lane);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < F::STAGES; ++i) prod.issue(P, held, ring + i * F::REC, bars + i, 1u << i, lane);
 
         Warp<F> w;
@@ -918,10 +920,8 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                 const Place at = get(held.at);
                 n = min(at.sp.n - at.t, todo);
                 p0 = (at.sp.tile0 + at.t) * kGroup;
-                if (!nothing(at.sp)) {
-                    w.load_queries(P, at, held, lane);
-                    w.start();
-                }
+                w.start();
+                if (!nothing(at.sp)) w.load_queries(P, at, held, lane);
             }
             for (int i = n; i > 0; --i) {
                 const uint32_t stage = used % F::STAGES;
@@ -946,10 +946,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
             const bool whole = n == at.sp.n;
             todo -= n;
             const int row0 = at.rt * F::RC;
-            if (nothing(at.sp)) {
-                for (int row = row0; row < min(row0 + F::RC, P.rows); ++row)
-                    RowSum<F>().write(P, at.s, row_of(P, at.sp.len, at.sp.nl, at.h, row), 0.0f, 0.0f, lane);
-            } else if (whole) {
+            if (whole) {
                 struct To {
                     int64_t at;
                     float inv;
@@ -1003,6 +1000,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
         const int mine_part = valid ? ents[lane].part : 0;
         uint32_t rest = __ballot_sync(kFull, valid);
         int task = warp;
+#pragma unroll 1
         while (rest) {
             const int e0 = __ffs(rest) - 1;
             const Entry en = ents[e0];
@@ -1013,6 +1011,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
             if (!whole && tid == 0) cut_entry[slot] = e0;
             const int n = min(F::RC, P.rows - en.row0);
             const bool in = run_mask >> lane & 1;
+#pragma unroll 1
             for (; task < n; task += F::WARPS) {
                 const int row = task;
                 const float m = in ? ml[lane * 2 * F::RC + row] : kNoRef;
@@ -1021,7 +1020,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                 const float k = in ? weight(m, top) : 0.0f;
                 l = warp_sum(in ? k * l : 0.0f);
                 RowSum<F> sum;
-#pragma unroll 4
+#pragma unroll 1
                 for (uint32_t left = run_mask; left; left &= left - 1) {
                     const int e = __ffs(left) - 1;
                     sum.template add<false>(reinterpret_cast<const float*>(smem) + __shfl_sync(kFull, mine_part, e) + row * F::ROW,
@@ -1064,8 +1063,8 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
         if (!joins[k]) continue;
         const Entry en = ents[cut_entry[k]];
         const int i0 = cp.of(en.start), i1 = cp.of(en.start + en.n - 1);
-        const float* const part0 = P.parts + (i0 * 2 + (en.start > cp.begin(i0))) * F::WPART;  // the other CTAs': in their first slot
-        auto part = [&](int i) { return i == 0 ? part0 : P.parts + (i0 + i) * 2 * F::WPART; };
+        // the unit's first CTA may have it in its second slot, the others have it in their first
+        const int shift = en.start > cp.begin(i0) ? F::WPART : 0;
         // chunks of parts by warp, all loads of one in flight at once; the chunks' sums meet in
         // the rings' memory
         const int n = i1 - i0 + 1, nrows = min(F::RC, P.rows - en.row0);
@@ -1073,24 +1072,30 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
         const int chunks = (n + per - 1) / per;
         float* const sums = reinterpret_cast<float*>(smem);  // [chunk][row][DIM sums, ref, l]
         if (k == 1 && joins[0]) __syncthreads();
+#pragma unroll 1
         for (int task = warp, chunk = 0; chunk < chunks; task -= nrows, ++chunk)
+#pragma unroll 1
             for (; task < nrows; task += F::WARPS) {
                 const int row = task, c0 = chunk * per, m = min(per, n - c0);
+                const float* const from = P.parts + (i0 + c0) * 2 * F::WPART + row * F::DIM;
+                const int first = c0 == 0 ? shift : 0;
                 float ref = kNoRef, l = 0.0f;
                 if (lane < m) {
-                    const float* const q = part(c0 + lane) + F::RC * F::DIM + row;
+                    const float* const q = from + lane * 2 * F::WPART + (lane == 0 ? first : 0) + (F::RC - row) * F::DIM + row;
                     ref = __ldcg(q), l = __ldcg(q + F::RC);
                 }
                 RowSum<F> sum, v[8];
+                v[0].load(from + first, lane);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < m) v[i].load(part(c0 + i) + row * F::DIM, lane);
+                for (int i = 1; i < 8; ++i)
+                    if (i < m) v[i].load(from + i * 2 * F::WPART, lane);
                 const float top = warp_max(ref);
                 const float w = lane < m ? weight(ref, top) : 0.0f;
                 l = warp_sum(l * w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum.add(v[i], __shfl_sync(kFull, w, i));
-                for (int i = 8; i < m; ++i) sum.template add<true>(part(c0 + i) + row * F::DIM, __shfl_sync(kFull, w, i), lane);
+#pragma unroll 1
+                for (int i = 8; i < m; ++i) sum.template add<true>(from + i * 2 * F::WPART, __shfl_sync(kFull, w, i), lane);
                 if (chunks == 1) {
                     sum.write(P, en.s, row_of(P, en.len, en.nl, en.h, en.row0 + row), top, l, lane);
                 } else {
@@ -1101,6 +1106,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
             }
         if (chunks == 1) continue;
         __syncthreads();
+#pragma unroll 1
         for (int row = warp; row < nrows; row += F::WARPS) {
             const float* const from = sums + row * (F::DIM + 4);
             const int stride = nrows * (F::DIM + 4);
@@ -1109,6 +1115,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
             const float top = warp_max(ref), w = lane < chunks ? weight(ref, top) : 0.0f;
             l = warp_sum(w * l);
             RowSum<F> sum;
+#pragma unroll 1
             for (int i = 0; i < chunks; ++i) sum.template add<false>(from + i * stride, __shfl_sync(kFull, w, i), lane);
             sum.write(P, en.s, row_of(P, en.len, en.nl, en.h, en.row0 + row), top, l, lane);
         }

@@ -102,6 +102,7 @@ struct AttnParams {
     int32_t group, rows;   // query heads of a key/value head; times tokens
     uint32_t group_inv;    // ceil(2^32 / group), 0 for a group of 1
     int32_t rpp;           // records of a page
+    uint32_t tx_extra;     // 0; a test's waits expect so many bytes more than come
     int32_t rt_count, units;  // row tiles of a key/value head, units of a sequence: set at the launch
 };
 

@@ -319,3 +319,27 @@ def test_capture_without_a_workspace():
                 graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, F32), (128, BF16), (256, F16)])
+def test_waits_run_out_and_the_device_stays_usable(dim, dtype):
+    """Barriers that expect more than comes: the kernel gives up, records it, and ends; the
+    same workspace, cleared, serves a normal call."""
+    import ctypes
+    f = Filled([700, 0, 40], 2, dim, 32, seed=50)
+    q = queries(3, 1, 4, dim, dtype, seed=51)
+    ws = q4.workspace(q4.kv_attention_workspace_bytes(dim))
+    out = torch.empty_like(q)
+    r = ctypes.byref
+    seqs = q4._kv_seqs(f.cache, f.table, f.lens, None)
+    rows = [q4._kv_rows(f.cache, t, tuple(q.shape), "q") for t in (q, out)]
+    call = q4.lib().q4_debug_kv_attention_stall
+    call.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32] + [ctypes.c_void_p] * 4 + [ctypes.c_size_t, ctypes.c_void_p]
+    call.restype = ctypes.c_int
+    scores = q4.q4_kv_scores(0.1, 0.0, 0, None)
+    assert call(r(f.cache.c), r(seqs), 1, 4, r(rows[0]), r(scores), r(rows[1]), ws.data_ptr(), ws.numel(), None) == 0
+    torch.cuda.synchronize()
+    assert q4.workspace_status(ws) == 6
+    q4.workspace_init(ws)
+    check_attention(f, q, ws=ws)
+    assert q4.workspace_status(ws) == 0
