@@ -9,26 +9,47 @@
 // codes have to be unpacked, and at the HBM rate an SM has about three lane-instructions
 // for each code. So the kernel is built around instructions per code:
 //  - The products run on m16n8k16 tensor-core steps with the codes as the A operand and
-//    the query rows as the eight columns of B, so that few rows waste little. A nibble
-//    masked in place (bits 0-3 or 4-7 of a 16-bit half) IS the binary16 subnormal
-//    q * 2^-24 or q * 2^-20, exactly: one logic operation makes two operands. The offset
-//    of 8 never touches a code: it enters the scores as -8 * sum(q row) per block, in the
-//    accumulator's initial value, and the outputs as -8 * sum(weights), which one
-//    more tensor-core step a block sums from the very weights that the products use.
+//    the query rows as the eight columns of B, so that few rows waste little. (tcgen05 has
+//    128 rows of codes to an instruction too, but takes them from tensor or shared memory:
+//    the unpacked codes would be written and, for the values, transposed on the way, and
+//    the products themselves are 25% of the tensor pipe here.)
+//  - bfloat16 rows: a nibble masked in place (bits 0-3 or 4-7 of a 16-bit half) IS the
+//    binary16 subnormal q * 2^-24 or q * 2^-20, exactly: one logic operation makes two
+//    operands. The offset of 8 never touches a code: it enters the scores as
+//    -8 * sum(query row over a block) times the key scale, one small product, and the outputs
+//    as -8 * sum(weights), which one more tensor-core step a block sums from the very weights that
+//    the products use.
 //  - The cache's layout puts each lane's operands into one 16-byte shared load (keys by
 //    word, values by token pairs), a record of 32 tokens into one bulk copy.
 //  - The key scale multiplies a block's accumulator in binary32; the value scale
 //    multiplies the weights.
 //  - Softmax keeps a reference per row instead of the exact running maximum: weights
-//    are 2^(x - ref), and ref moves only when a weight times a value scale could pass
-//    2^15 (the test is one vote a tile), leaving 5 bits of room.
-// Rounding. binary32 and binary16 queries (and results): each query row, scaled by a power
-// of two, and each weight times its scale are held as two binary16 parts (22 bits),
-// neighbouring columns of B. bfloat16 queries with bfloat16 results: one part each (the
-// query's 8 bits are exact; weights and their product with the scale round to binary16's
-// 2^-11 twice, an eighth of the result's own last place... each).
+//    are 2^(x - ref), and ref moves only when a weight or a weight times a value scale could
+//    pass 2^15 (the test is one vote a record), leaving 5 bits of room.
+//  - Code that is run once a launch costs its instruction fetches (about 30 cycles an
+//    instruction were seen), so the row types are template parameters, the host computes what
+//    it can, and cold loops are not unrolled: that alone took 10 us calls to 9 and 16 us
+//    ones to 13.
 //
-// One CTA an SM; each warp streams its own tiles through its own ring of records.
+// Rounding. bfloat16 queries with bfloat16 results: a query's 8 bits are exact in binary16
+// once its row is scaled by a power of two (elements below 2^-27 of the largest round); a
+// weight rounds to binary16's 2^-11, and once more times its scale: together an eighth of
+// what the result's own rounding may add. All other types: each scaled query row, and each
+// weight times its scale, is held as two binary16 parts (22 bits), neighbouring columns of
+// B, and the codes become the exact normal numbers q - 8 by one more operation, because the tensor
+// core aligns products by the nominal exponent of a subnormal (which was seen to cost 4e-6 of
+// the result; with normal operands the results are within 3e-7 of binary64). Scores, sums
+// and references are binary32 everywhere.
+//
+// Work: see q4_kv_plan.h. One CTA an SM; each warp streams its own tiles through its own ring
+// of two records (three and four measured the same).
+//
+// Measured on a B200 (device time): 16 sequences of up to 32768 tokens, 32 query heads on 8
+// of 128, bfloat16: 66 us, 285 MB, 4.3 TB/s (67% of the measured copy rate; the same with every
+// byte in L2: 64 us; without the products: 56 us); in binary32 77 us. 550 instructions a record, of
+// which 192 unpack, 80 are products, 64 apply key scales. One sequence of 8192 tokens: 13 us;
+// of 777, 3 heads of 64: 9 us. Per launch: about 2 us to find a warp's work and its page,
+// 1.5 us to lay the queries out, 5 us to join what warps and CTAs cut.
 #pragma once
 
 #include <cuda_bf16.h>
