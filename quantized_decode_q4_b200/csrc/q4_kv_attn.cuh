@@ -117,6 +117,13 @@ struct Entry {
     int32_t part;          // float offset in shared memory, -1: none
 };
 static_assert(sizeof(Entry) == 32, "entry");
+
+// A unit that a CTA shares with others: its first unit (slot 0) or its last.
+struct Cut {
+    int32_t s, h, row0, len, nl;  // as an entry's
+    int32_t first, count;         // the CTAs that have parts of it
+    int32_t shift;                // floats from the first one's slot 0 to the one it uses
+};
 static_assert(16 * kJoin >= kMaxCtas, "chunks");
 
 __device__ __forceinline__ float ex2(float x) {
@@ -827,7 +834,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 template <class F>
 __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __grid_constant__ AttnParams P) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int cut_entry[2], joins[2];  // units that this CTA shares with others: its first, its last
+    __shared__ Cut cuts[2];
+    __shared__ int joins[2];  // slot i: 0 no unit is cut there, 1 one is, 2 this CTA joins it
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float* const parts = reinterpret_cast<float*>(smem + F::OFF_PART);
     float* const ml = reinterpret_cast<float*>(smem + F::OFF_ML);  // [warp][first, last][ref, l][RC]
@@ -848,7 +856,6 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
         q4dev::mbar_fence_init();
         ents[2 * warp].part = ents[2 * warp + 1].part = -1;
     }
-    if (tid < 2) cut_entry[tid] = -1;
     int all, before = 0;  // few: tiles before the lane's sequence
     {
         int sum = mine.n;
@@ -884,8 +891,18 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
     const Parts cp(total, ctas);
     const int a = cp.begin(blockIdx.x), z = cp.begin(blockIdx.x + 1);
     const Parts wp(z - a, F::WARPS);
+    // Notes whether the CTA's range cuts its first (slot 0) or its last unit: the warp that has
+    // the range's first or last tile writes that slot. The last unit may be the first.
+    auto note_cut = [&](int slot, const Place& at, int start) {
+        const bool cut = (start < a || start + at.sp.n > z) && slot == (start > a);
+        joins[slot] = cut;
+        if (!cut) return;
+        const int i0 = cp.of(start);
+        cuts[slot] = {at.s, at.h, at.rt * F::RC, at.sp.len, at.sp.nl, i0, cp.of(start + at.sp.n - 1) - i0 + 1, start > cp.begin(i0) ? F::WPART : 0};
+    };
     const int wa = a + wp.begin(warp);
-    int todo = wp.q + (warp < wp.r);
+    const int mine_tiles = wp.q + (warp < wp.r);
+    int todo = mine_tiles;
 
     if (todo > 0) {
         // the place of tile wa
@@ -932,6 +949,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
 #pragma unroll 1
         for (int i = 0; i < F::STAGES; ++i) prod.issue(P, held, ring + i * F::REC, bars + i, 1u << i, lane);
 
+        if (tid == 0) note_cut(0, get(held.at), held.start);
         Warp<F> w;
         uint32_t used = 0, phases = 0;  // tiles done; bit i: parity of the next wait on stage i
         bool dead = false;
@@ -1003,6 +1021,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
                     e.part = (int)(p - reinterpret_cast<float*>(smem));
                 }
             }
+            if (lane == 0 && todo == 0 && wa + mine_tiles == z) note_cut(1, at, held.start);
             if (todo > 0) {
                 held.start = held.start + at.sp.n;
                 next_unit(P, at);
@@ -1029,7 +1048,6 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
             rest &= ~run_mask;
             const bool whole = en.start >= a && en.start + en.n <= z;
             const int slot = en.start > a;
-            if (!whole && tid == 0) cut_entry[slot] = e0;
             const int n = min(F::RC, P.rows - en.row0);
             const bool in = run_mask >> lane & 1;
 #pragma unroll 1
@@ -1059,47 +1077,40 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
         }
     }
     __syncthreads();
-    if (cut_entry[0] < 0 && cut_entry[1] < 0) return;
+    if (!(joins[0] | joins[1])) return;
     // and those that CTAs cut: the last to arrive joins them in order
-    if (tid < 2) {
-        int join = 0;
-        if (cut_entry[tid] >= 0) {
-            const Entry& en = ents[cut_entry[tid]];
-            const int i0 = cp.of(en.start), i1 = cp.of(en.start + en.n - 1);
-            const int sh = 8 * (i0 & 3);
-            uint32_t* const ticket = P.ws + 1 + (i0 >> 2);
-            __threadfence();
-            const uint32_t old = atomicAdd(ticket, 1u << sh);
-            if ((int)(old >> sh & 255u) == i1 - i0) {
-                atomicSub(ticket, (uint32_t)(i1 - i0 + 1) << sh);
-                __threadfence();
-                join = 1;
-            }
+    __syncthreads();
+    if (tid < 2 && joins[tid]) {
+        const Cut& cut = cuts[tid];
+        const int sh = 8 * (cut.first & 3);
+        uint32_t* const ticket = P.ws + 1 + (cut.first >> 2);
+        // releases what the barrier has made this thread see, acquires what the others released
+        uint32_t old;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(ticket), "r"(1u << sh) : "memory");
+        if ((int)(old >> sh & 255u) == cut.count - 1) {
+            atomicSub(ticket, (uint32_t)cut.count << sh);
+            joins[tid] = 2;
         }
-        joins[tid] = join;
     }
     __syncthreads();
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
-        if (!joins[k]) continue;
-        const Entry en = ents[cut_entry[k]];
-        const int i0 = cp.of(en.start), i1 = cp.of(en.start + en.n - 1);
-        // the unit's first CTA may have it in its second slot, the others have it in their first
-        const int shift = en.start > cp.begin(i0) ? F::WPART : 0;
+        if (joins[k] != 2) continue;
+        const Cut en = cuts[k];
         // chunks of parts by warp, all loads of one in flight at once; the chunks' sums meet in
         // the rings' memory
-        const int n = i1 - i0 + 1, nrows = min(F::RC, P.rows - en.row0);
+        const int n = en.count, nrows = min(F::RC, P.rows - en.row0);
         const int per = n <= 8 * kJoin ? 8 : 16;
         const int chunks = (n + per - 1) / per;
         float* const sums = reinterpret_cast<float*>(smem);  // [chunk][row][DIM sums, ref, l]
-        if (k == 1 && joins[0]) __syncthreads();
+        if (k == 1 && joins[0] == 2) __syncthreads();
 #pragma unroll 1
         for (int task = warp, chunk = 0; chunk < chunks; task -= nrows, ++chunk)
 #pragma unroll 1
             for (; task < nrows; task += F::WARPS) {
                 const int row = task, c0 = chunk * per, m = min(per, n - c0);
-                const float* const from = P.parts + (i0 + c0) * 2 * F::WPART + row * F::DIM;
-                const int first = c0 == 0 ? shift : 0;
+                const float* const from = P.parts + (en.first + c0) * 2 * F::WPART + row * F::DIM;
+                const int first = c0 == 0 ? en.shift : 0;
                 float ref = kNoRef, l = 0.0f;
                 if (lane < m) {
                     const float* const q = from + lane * 2 * F::WPART + (lane == 0 ? first : 0) + (F::RC - row) * F::DIM + row;
