@@ -85,7 +85,7 @@ def test_attention_refusals():
         assert call(scores=sc) == INVALID, sc
     # more query heads a key/value head, or more tiles, than the kernel counts
     assert call(heads=2 * 4097) == INVALID
-    assert call(s=seqs(pages=(1 << 26) - 1, count=16)) == INVALID and call(s=seqs(pages=1 << 20, count=1 << 10), tokens=16) == INVALID
+    assert call(s=seqs(pages=(1 << 26) - 1, count=17)) == INVALID and call(s=seqs(pages=1 << 20, count=1 << 10), tokens=16) == INVALID
     assert call(scores=(1, 0, 0, 258)) == MISALIGNED and call(lse=258) == MISALIGNED
     assert call(q=None) == INVALID and call(out=None) == INVALID and call(q=rows(type=7)) == UNSUPPORTED
     assert call(out=rows(h=0)) == INVALID and call(out=rows(t=0)) == INVALID
