@@ -241,7 +241,8 @@ struct Place {
 };
 
 // What a warp looks at where a page, a unit or a sequence ends is held in shared memory: its
-// loop needs the registers. Every lane writes and reads the same values.
+// loop needs the registers. Every lane writes and reads the same values; a warp barrier stands
+// between what is read and what overwrites it, and before the next reading.
 struct Held {
     int start;                 // first tile of the unit that the warp works on
     Place at;                  // and its place
@@ -740,10 +741,10 @@ struct Producer {
         --left;
         if (--run == 0 && left > 0) {
             Place at = get(held.next);
-            const int unit = held.unit_left;
+            const int unit = held.unit_left, page = held.page + 1;
+            int base = held.base;
+            __syncwarp();
             if (unit > 0) {
-                const int page = held.page + 1;
-                int base = held.base;
                 if (page - base == 32) load_entries(P, at.s, base = page, lane);
                 open(P, held, at, page, base, 0, unit, lane);
             } else {
@@ -1027,9 +1028,12 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
             }
             if (lane == 0 && todo == 0 && wa + mine_tiles == z) note_cut(1, at, held.start);
             if (todo > 0) {
-                held.start = held.start + at.sp.n;
+                const int start = held.start + at.sp.n;
+                __syncwarp();
+                held.start = start;
                 next_unit(P, at);
                 put(held.at, at);
+                __syncwarp();
             }
         }
         if (dead && lane == 0) atomicOr(P.ws, kTimeoutFlag);

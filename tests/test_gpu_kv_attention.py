@@ -343,3 +343,14 @@ def test_waits_run_out_and_the_device_stays_usable(dim, dtype):
     q4.workspace_init(ws)
     check_attention(f, q, ws=ws)
     assert q4.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("count,dim,tokens", [(32, 128, 1), (33, 64, 3), (200, 128, 1), (513, 256, 2)])
+def test_batches_of_every_kind_of_count(count, dim, tokens):
+    """Up to 32 sequences each warp finds its work by itself, above that the CTA does, a
+    thread a sequence or several; every third holds nothing."""
+    g = torch.Generator().manual_seed(count)
+    lens = [0 if i % 3 == 1 else int(v) for i, v in enumerate(torch.randint(0, 200, (count,), generator=g))]
+    f = Filled(lens, 2, dim, 32, seed=count)
+    for dtype in (F32, BF16):
+        check_attention(f, queries(count, tokens, 6, dim, dtype, seed=count))
