@@ -355,6 +355,25 @@ q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int3
                           const q4_rows* q, const q4_kv_scores* scores, const q4_rows* out, float* lse,
                           void* ws, size_t ws_bytes, void* stream);
 
+/* The arguments of the three calls in one structure, for bindings in which every argument
+ * costs: q4_kv_call(0, ..) is q4_kv_write with a = k and b = v, q4_kv_call(1, ..) q4_kv_read with
+ * a = k, b = v and extra = starts, q4_kv_call(2, ..) q4_kv_attention with a = q, b = out and
+ * extra = lse. Members that a call has no use for are ignored. The same checks, the same
+ * errors; Q4_ERR_INVALID_ARG for another number. */
+typedef struct {
+    q4_kv_cache cache;
+    q4_kv_seqs seqs;
+    q4_rows a;
+    q4_rows b;
+    q4_kv_scores scores;
+    void* extra;
+    void* ws;
+    size_t ws_bytes;
+    int32_t tokens;
+    int32_t q_heads;
+} q4_kv_args;
+q4_status q4_kv_call(int which, const q4_kv_args* args, void* stream);
+
 /* A static, human-readable name for a status code. */
 const char* q4_status_string(q4_status s);
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -107,6 +108,7 @@ def lib():
             "q4_kv_cache_bytes": ([i64, i32, i32, i32], sz),
             "q4_kv_write": ([vp, vp, i32, vp, vp, vp], c.c_int),
             "q4_kv_read": ([vp, vp, vp, i32, vp, vp, vp], c.c_int),
+            "q4_kv_call": ([c.c_int, c.c_char_p, vp], c.c_int),
             "q4_kv_attention_workspace_bytes": ([i32], sz),
             "q4_kv_attention": ([vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp], c.c_int),
         }
@@ -317,6 +319,7 @@ class KVCache:
         self.pages, self.heads, self.dim, self.page_size = pages, heads, dim, page_size
         self.data, self.device, self.index = data, data.device, data.device.index
         self.c = q4_kv_cache(data.data_ptr(), pages, heads, dim, page_size)
+        self.packed = struct.pack("@Pqiii4x", data.data_ptr(), pages, heads, dim, page_size)
 
     @property
     def nbytes(self) -> int:
@@ -333,9 +336,14 @@ def kv_cache_bytes(pages: int, heads: int, dim: int, page_size: int) -> int:
 
 
 # The calls below take a few microseconds on the GPU, so their checks are kept to what a
-# wrong argument could not do without, in few Python operations.
+# wrong argument could not do without, in few Python operations, and their arguments go over
+# in one packed structure (q4_kv_args: the cache, then these).
+_ARGS = struct.Struct("@PqiiPP" "Pi4xqqq" "Pi4xqqq" "ffi4xP" "PPNii")
+_NO_SCORES = (0.0, 0.0, 0, 0)
 
-def _kv_seqs(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_lens) -> q4_kv_seqs:
+
+def _seqs_args(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_lens) -> tuple:
+    """The members of q4_kv_seqs; the count is the fourth."""
     i32, dev = torch.int32, cache.device
     shape, stride = table.shape, table.stride()
     if (len(shape) != 2 or table.dtype is not i32 or table.device != dev or shape[1] == 0
@@ -344,23 +352,40 @@ def _kv_seqs(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_lens) 
     n = shape[0]
     if lens.dtype is not i32 or lens.shape != (n,) or lens.device != dev or not lens.is_contiguous():
         raise Q4Error(1, "lens")
-    if new_lens is not None:
+    if new_lens is None:
+        new_lens = 0
+    else:
         if (new_lens.dtype is not i32 or new_lens.shape != (n,) or new_lens.device != dev
                 or not new_lens.is_contiguous()):
             raise Q4Error(1, "new_lens")
         new_lens = new_lens.data_ptr()
-    return q4_kv_seqs(table.data_ptr(), stride[0], shape[1], n, lens.data_ptr(), new_lens)
+    return table.data_ptr(), stride[0], shape[1], n, lens.data_ptr(), new_lens
 
 
-def _kv_rows(cache: KVCache, t: torch.Tensor, shape: tuple, what: str) -> q4_rows:
-    """The rows `t` of the given [seqs][tokens][heads][dim]."""
+def _rows_args(cache: KVCache, t: torch.Tensor, shape: tuple, what: str) -> tuple:
+    """The members of q4_rows for the rows `t` of the given [seqs][tokens][heads][dim]."""
     code = _TYPES.get(t.dtype)
     if code is None or t.shape != shape or t.device != cache.device:
         raise Q4Error(1, what)
     a, b, c, d = t.stride()
     if d != 1:
         raise Q4Error(1, what)
-    return q4_rows(t.data_ptr(), code, a, b, c)
+    return t.data_ptr(), code, a, b, c
+
+
+def _kv_seqs(cache: KVCache, table, lens, new_lens) -> q4_kv_seqs:
+    return q4_kv_seqs(*_seqs_args(cache, table, lens, new_lens))
+
+
+def _kv_rows(cache: KVCache, t: torch.Tensor, shape: tuple, what: str) -> q4_rows:
+    return q4_rows(*_rows_args(cache, t, shape, what))
+
+
+def _kv_call(which: int, cache: KVCache, args: bytes, where: str) -> None:
+    status = (_lib or lib()).q4_kv_call(which, cache.packed + args,
+                                        torch._C._cuda_getCurrentRawStream(cache.index))
+    if status:
+        _check(status, where)
 
 
 def _elsewhere(cache: KVCache, stream) -> bool:
@@ -385,17 +410,13 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tens
     without a place are skipped. The positions of a call have to be distinct."""
     if _elsewhere(cache, stream):
         return _there(cache, stream, lambda: kv_write(cache, k, v, table, lens, new_lens))
-    seqs = _kv_seqs(cache, table, lens, new_lens)
-    n, tokens = seqs.count, k.shape[1] if k.dim() == 4 else 0
+    seqs = _seqs_args(cache, table, lens, new_lens)
+    n, tokens = seqs[3], k.shape[1] if k.dim() == 4 else 0
     shape = (n, tokens, cache.heads, cache.dim)
-    ck, cv = _kv_rows(cache, k, shape, "k"), _kv_rows(cache, v, shape, "v")
+    ck, cv = _rows_args(cache, k, shape, "k"), _rows_args(cache, v, shape, "v")
     if tokens == 0 or n == 0:
         return
-    r = ctypes.byref
-    status = lib().q4_kv_write(r(cache.c), r(seqs), tokens, r(ck), r(cv),
-                               torch._C._cuda_getCurrentRawStream(cache.index))
-    if status:
-        _check(status, "q4_kv_write")
+    _kv_call(0, cache, _ARGS.pack(*seqs, *ck, *cv, *_NO_SCORES, 0, 0, 0, tokens, 0), "q4_kv_write")
 
 
 def kv_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, tokens: int,
@@ -405,25 +426,27 @@ def kv_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, tokens: int
     out: the pair to write instead of new tensors of `dtype`."""
     if _elsewhere(cache, stream):
         return _there(cache, stream, lambda: kv_read(cache, table, lens, tokens, starts, dtype, out))
-    seqs = _kv_seqs(cache, table, lens, None)
-    n = seqs.count
+    seqs = _seqs_args(cache, table, lens, None)
+    n = seqs[3]
     if starts is not None:
         _require(starts.dtype is torch.int32 and starts.shape == (n,)
                  and starts.device == cache.device and starts.is_contiguous(), "starts")
-    _require(0 <= tokens < 2**31 and (out is not None or dtype in _TYPES), "tokens or dtype")
-    shape = (n, tokens, cache.heads, cache.dim)
+    heads, dim = cache.heads, cache.dim
+    shape = (n, tokens, heads, dim)
     if out is None:
+        code = _TYPES.get(dtype)
+        if code is None or not 0 <= tokens < 2**31:
+            raise Q4Error(1, "tokens or dtype")
         k = cache.data.new_empty(shape, dtype=dtype)
         v = torch.empty_like(k)
+        rows = (code, tokens * heads * dim, heads * dim, dim)
+        ck, cv = (k.data_ptr(), *rows), (v.data_ptr(), *rows)
     else:
         k, v = out
-    ck, cv = _kv_rows(cache, k, shape, "k"), _kv_rows(cache, v, shape, "v")
+        ck, cv = _rows_args(cache, k, shape, "k"), _rows_args(cache, v, shape, "v")
     if tokens and n:
-        r = ctypes.byref
-        status = lib().q4_kv_read(r(cache.c), r(seqs), None if starts is None else starts.data_ptr(),
-                                  tokens, r(ck), r(cv), torch._C._cuda_getCurrentRawStream(cache.index))
-        if status:
-            _check(status, "q4_kv_read")
+        _kv_call(1, cache, _ARGS.pack(*seqs, *ck, *cv, *_NO_SCORES, 0 if starts is None else starts.data_ptr(),
+                                      0, 0, tokens, 0), "q4_kv_read")
     return k, v
 
 
@@ -451,35 +474,39 @@ def kv_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, lens: tor
     if _elsewhere(cache, stream):
         return _there(cache, stream, lambda: kv_attention(cache, q, table, lens, new_lens, scale, window,
                                                           softcap, alibi, out, lse, ws))
-    seqs = _kv_seqs(cache, table, lens, new_lens)
+    seqs = _seqs_args(cache, table, lens, new_lens)
     shape = q.shape
     _require(len(shape) == 4, "q")
-    n, tokens, heads = seqs.count, shape[1], shape[2]
-    cq = _kv_rows(cache, q, (n, tokens, heads, cache.dim), "q")
-    _require(0 <= window < 2**31, "window")
-    scores = q4_kv_scores(cache.dim ** -0.5 if scale is None else scale, softcap, window, None)
+    n, tokens, heads = seqs[3], shape[1], shape[2]
+    cq = _rows_args(cache, q, (n, tokens, heads, cache.dim), "q")
+    _require(0 <= window < 2**31 and heads < 2**31, "window")
+    slopes = sums = 0
     if alibi is not None:
         _require(alibi.dtype is torch.float32 and alibi.shape == (heads,) and alibi.is_contiguous()
                  and alibi.device == cache.device, "alibi")
-        scores.alibi = alibi.data_ptr()
+        slopes = alibi.data_ptr()
     if lse is not None:
         _require(lse.dtype is torch.float32 and lse.shape == (n, tokens, heads) and lse.is_contiguous()
                  and lse.device == cache.device, "lse")
-        lse = lse.data_ptr()
-    if out is None:
-        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
-    co = _kv_rows(cache, out, shape, "out")
+        sums = lse.data_ptr()
+    if out is None and q.is_contiguous():
+        out = torch.empty_like(q)
+        co = (out.data_ptr(), *cq[1:])
+    else:
+        out = q.new_empty(shape) if out is None else out
+        co = _rows_args(cache, out, shape, "out")
     if tokens == 0 or n == 0:
         return out
     if ws is None:
         ws = workspace(kv_attention_workspace_bytes(cache.dim), cache.device)
     elif ws.dtype is not torch.uint8 or ws.device != cache.device or not ws.is_contiguous():
         raise Q4Error(1, "ws")
-    r = ctypes.byref
-    status = lib().q4_kv_attention(r(cache.c), r(seqs), tokens, heads, r(cq), r(scores), r(co), lse,
-                                   ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(cache.index))
-    if status:
-        _check(status, "q4_kv_attention")
+    try:
+        args = _ARGS.pack(*seqs, *cq, *co, cache.dim ** -0.5 if scale is None else scale, softcap, window,
+                          slopes, sums, ws.data_ptr(), ws.numel(), tokens, heads)
+    except OverflowError:  # a scale or cap that is no binary32 number
+        raise Q4Error(1, "scale or softcap") from None
+    _kv_call(2, cache, args, "q4_kv_attention")
     return out
 
 

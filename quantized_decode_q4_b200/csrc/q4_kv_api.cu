@@ -179,6 +179,18 @@ q4_status q4_kv_attention(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int3
     return attention_call(cache, seqs, tokens, q_heads, q, scores, out, lse, ws, ws_bytes, stream, 0u);
 }
 
+q4_status q4_kv_call(int which, const q4_kv_args* a, void* stream) {
+    if (!a) return Q4_ERR_INVALID_ARG;
+    switch (which) {
+        case 0: return q4_kv_write(&a->cache, &a->seqs, a->tokens, &a->a, &a->b, stream);
+        case 1: return q4_kv_read(&a->cache, &a->seqs, static_cast<const int32_t*>(a->extra), a->tokens, &a->a, &a->b, stream);
+        case 2:
+            return q4_kv_attention(&a->cache, &a->seqs, a->tokens, a->q_heads, &a->a, &a->scores, &a->b,
+                                   static_cast<float*>(a->extra), a->ws, a->ws_bytes, stream);
+    }
+    return Q4_ERR_INVALID_ARG;
+}
+
 q4_status q4_debug_kv_attention_stall(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t tokens, int32_t q_heads,
                                       const q4_rows* q, const q4_kv_scores* scores, const q4_rows* out, void* ws,
                                       size_t ws_bytes, void* stream) {

@@ -138,3 +138,36 @@ def test_attention_plans_replay_on_host():
         window = 0 if rng.random() < 0.5 else int(2 ** rng.uniform(0, 14))
         reach = -(-max(1, top if rng.random() < 0.8 else top // 2) // 32) * 32
         check(lens, new, tokens, window, reach, int(rng.integers(1, 40)), int(rng.choice([8, 12, 16])), int(rng.choice([148, 3, 252])))
+
+
+def test_packed_arguments_are_the_structure():
+    """q4_kv_call takes what the binding packs: the calls' own refusals come back."""
+    import struct
+
+    L = q4.lib()
+
+    class Args(ctypes.Structure):
+        _fields_ = [("cache", q4.q4_kv_cache), ("seqs", q4.q4_kv_seqs), ("a", q4.q4_rows), ("b", q4.q4_rows), ("scores", q4.q4_kv_scores),
+                    ("extra", ctypes.c_void_p), ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t), ("tokens", ctypes.c_int32),
+                    ("q_heads", ctypes.c_int32)]
+
+    head = struct.pack("@Pqiii4x", 1, 2, 3, 4, 5)
+    rest = q4._ARGS.pack(6, 7, 8, 9, 10, 11, 12, 2, 13, 14, 15, 16, 1, 17, 18, 19, 0.5, 0.25, 20, 21, 22, 23, 24, 25, 26)
+    assert len(head) + len(rest) == ctypes.sizeof(Args)
+    a = Args.from_buffer_copy(head + rest)
+    assert (a.cache.data, a.cache.pages, a.cache.heads, a.cache.dim, a.cache.page_size) == (1, 2, 3, 4, 5)
+    assert (a.seqs.table, a.seqs.table_stride, a.seqs.table_pages, a.seqs.count, a.seqs.lens, a.seqs.new_lens) == (6, 7, 8, 9, 10, 11)
+    assert [(r.data, r.type, r.seq_stride, r.token_stride, r.head_stride) for r in (a.a, a.b)] == [(12, 2, 13, 14, 15), (16, 1, 17, 18, 19)]
+    assert (a.scores.scale, a.scores.softcap, a.scores.window, a.scores.alibi) == (0.5, 0.25, 20, 21)
+    assert (a.extra, a.ws, a.ws_bytes, a.tokens, a.q_heads) == (22, 23, 24, 25, 26)
+
+    def call(which, c=(256, 4, 2, 64, 32), tokens=2, ws=256, null=False):
+        need = q4.kv_attention_workspace_bytes(64)
+        b = struct.pack("@Pqiii4x", *c) + q4._ARGS.pack(256, 4, 4, 2, 256, 0, 256, 0, 512, 256, 64, 256, 0, 512, 256, 64, 0.125, 0.0, 0, 0,
+                                                        0, ws, need, tokens, 4)
+        return L.q4_kv_call(which, None if null else b, None)
+
+    for which in (0, 1, 2):
+        assert call(which, null=True) == INVALID and call(which, tokens=0) == 0
+        assert call(which, c=(256, 0, 2, 64, 32)) == INVALID and call(which, c=(192, 4, 2, 64, 32)) == MISALIGNED
+    assert call(2, tokens=17) == UNSUPPORTED and call(2, ws=0) == WORKSPACE and call(3) == INVALID and call(-1) == INVALID
