@@ -73,7 +73,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kTimeoutFlag = 1u;
 constexpr int kRoom = 5;  // bits that scores may rise after ref was set before it moves again
 constexpr uint32_t kOnes = 0x3c003c00u;  // binary16 (1, 1)
-constexpr int kNoWindow = INT32_MAX - 64;  // positions are above -64
+constexpr int kNoWindow = INT32_MAX - Q4_MAX_BATCH;  // rows stand at -15 .. 2^31 - 33: it hides nothing from them and their differences fit 32 bits
 constexpr int kJoin = 16;  // chunks of parts in a join; 16 parts each hold all CTAs
 constexpr float kNoRef = -1e30f;  // reference of a row that has seen nothing: finite, so that masked scores give weights of 0
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -1171,6 +1171,7 @@ template <class F>
 cudaError_t run(AttnParams P, int num_sms, cudaStream_t stream) {
     P.rt_count = (P.rows + F::RC - 1) / F::RC;
     P.units = P.cache.heads * P.rt_count;
+    if (P.window > kNoWindow) P.window = 0;
     const int grid = num_sms < kMaxCtas ? num_sms : kMaxCtas;
     kv_attention_kernel<F><<<grid, F::THREADS, F::SMEM, stream>>>(P);
     return cudaGetLastError();

@@ -1,4 +1,6 @@
 """Attention over the 4-bit key/value cache against the same in 64 bits."""
+import math
+
 import pytest
 import torch
 
@@ -354,3 +356,24 @@ def test_batches_of_every_kind_of_count(count, dim, tokens):
     f = Filled(lens, 2, dim, 32, seed=count)
     for dtype in (F32, BF16):
         check_attention(f, queries(count, tokens, 6, dim, dtype, seed=count))
+
+
+@pytest.mark.parametrize("window,visible", [(0, True), (2**31 - 1, True), (2**31 - 32, True), (2**31 - 33, False)])
+def test_the_longest_sequence(window, visible):
+    """2^31 - 32 tokens, nearly all of them one page's: token 0 outweighs the others wherever the
+    window shows it."""
+    cache = q4.KVCache(2, 1, 64, 32)
+    one = torch.ones(1, 32, 1, 64, device="cuda")
+    q4.kv_write(cache, 0 * one, one, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                torch.tensor([32], dtype=torch.int32, device="cuda"))
+    q4.kv_write(cache, one[:, :1], 2 * one[:, :1], torch.ones(1, 1, dtype=torch.int32, device="cuda"),
+                torch.tensor([1], dtype=torch.int32, device="cuda"))
+    table = torch.zeros(1, 2**26 - 1, dtype=torch.int32, device="cuda")
+    table[0, 0] = 1
+    lens = torch.tensor([2**31 - 32], dtype=torch.int32, device="cuda")
+    lse = torch.empty(1, 1, 1, device="cuda")
+    out = q4.kv_attention(cache, one[:, :1] * (100 / 64), table, lens, scale=1.0, window=window, lse=lse)
+    # hidden: scores of 0, values of 1 but for 31 of 0. Joins add 160 partial sums at most, of
+    # the outputs and of the weights, each to 2^-24: 2e-5
+    assert (out - (2.0 if visible else 1.0)).abs().max().item() < 2 * 2e-5
+    assert abs(lse.item() - (100.0 if visible else math.log(2**31 - 33))) < 2e-5 + 100 * 2**-23
