@@ -314,7 +314,7 @@ q4_status q4_kv_write(const q4_kv_cache* cache, const q4_kv_seqs* seqs, int32_t 
 /* q4_kv_read - expand positions starts[s] .. starts[s] + tokens - 1 (starts NULL: from
  * 0) of each sequence to dense rows, d * (q - 8) rounded once to the rows' type. Positions
  * below 0, at or behind lens[s], or without a page give zeros. seqs->new_lens is not used.
- * k, v, errors: as q4_kv_write (k and v are written). */
+ * k, v, errors: as q4_kv_write (k and v are written and may not overlap). */
 q4_status q4_kv_read(const q4_kv_cache* cache, const q4_kv_seqs* seqs, const int32_t* starts, int32_t tokens,
                      const q4_rows* k, const q4_rows* v, void* stream);
 
@@ -345,7 +345,10 @@ size_t q4_kv_attention_workspace_bytes(int32_t dim);
  * A query without a position, or with none that it sees, gets out = 0 and lse = -inf. Keys
  * whose table entry is outside the cache count as masked, and the workspace's status
  * (q4_workspace_status) becomes Q4_ERR_INVALID_ARG until it is zeroed. lens above the
- * table's reach count as that.
+ * table's reach count as that. The scales multiply whole products (of a query with a key's
+ * block, of a weight with a value's), so what a row makes of a block whose scale is
+ * infinite (values of 524,160 and above) is infinite or NaN where it sees it, or nothing
+ * where its score is minus infinity.
  * Scores, softmax and sums are binary32; see the kernel for what is rounded to fewer bits.
  * Errors: as q4_kv_write, Q4_ERR_WORKSPACE, Q4_ERR_UNSUPPORTED for tokens outside 0..16, and
  * Q4_ERR_INVALID_ARG for more than 4096 query heads a key/value head or for tables that could

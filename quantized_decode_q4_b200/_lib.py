@@ -317,9 +317,14 @@ class KVCache:
         _require(data.is_cuda and data.dtype == torch.uint8 and data.is_contiguous()
                  and data.numel() >= nbytes, "KVCache data")
         self.pages, self.heads, self.dim, self.page_size = pages, heads, dim, page_size
-        self.data, self.device, self.index = data, data.device, data.device.index
+        self._data, self.device, self.index = data, data.device, data.device.index
         self.c = q4_kv_cache(data.data_ptr(), pages, heads, dim, page_size)
         self.packed = struct.pack("@Pqiii4x", data.data_ptr(), pages, heads, dim, page_size)
+
+    @property
+    def data(self) -> torch.Tensor:
+        # no setter: the packed arguments hold its address
+        return self._data
 
     @property
     def nbytes(self) -> int:
@@ -437,7 +442,7 @@ def kv_read(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, tokens: int
         code = _TYPES.get(dtype)
         if code is None or not 0 <= tokens < 2**31:
             raise Q4Error(1, "tokens or dtype")
-        k = cache.data.new_empty(shape, dtype=dtype)
+        k = cache._data.new_empty(shape, dtype=dtype)
         v = torch.empty_like(k)
         rows = (code, tokens * heads * dim, heads * dim, dim)
         ck, cv = (k.data_ptr(), *rows), (v.data_ptr(), *rows)
@@ -468,7 +473,7 @@ def kv_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, lens: tor
     window > 0. Scores are scale * q . k (scale: 1 / sqrt(dim) if None), capped by
     softcap * tanh(score / softcap) if softcap > 0, plus alibi[head] * (key - query position)
     (alibi: binary32 [q_heads]). A query that sees nothing gets 0 and lse -inf.
-    out: the result, of q's type if None; lse: binary32 [seqs][tokens][q_heads] to fill;
+    out: the result, of q's type if None, not over q; lse: binary32 [seqs][tokens][q_heads] to fill;
     ws: a workspace of kv_attention_workspace_bytes(dim), one for each stream, else a new
     one for this call."""
     if _elsewhere(cache, stream):

@@ -277,3 +277,10 @@ def test_binding_refuses():
     refused(lambda: q4.kv_attention(cache, q, table, lens, ws=torch.zeros(16, dtype=torch.uint8, device="cuda")), 3)
     with pytest.raises(q4.Q4Error):
         q4.kv_attention_workspace_bytes(96)
+
+
+def test_the_memory_of_a_cache_is_not_exchanged():
+    cache = q4.KVCache(1, 1, 64, 32)
+    with pytest.raises(AttributeError):
+        cache.data = torch.zeros_like(cache.data)
+    assert cache.data.data_ptr() == cache.c.data and cache.data.numel() == cache.nbytes
