@@ -4,11 +4,13 @@
 // value is small, and by instructions until then. A warp takes a run of eight positions of one
 // head: its page is looked up once, and its codes are contiguous in the record (by chunk,
 // keys and values apart). (A warp a whole record reads as fast, but writes 8192 tokens of 8
-// heads in 57 us against 34: too few loads in flight.) Eight lanes own a block of 32 values,
-// four neighbours each, so that the dense side moves in coalesced 8- or 16-byte accesses. The
-// codes follow the rule of q4_pack bit for bit: every binary32 step is an explicit
+// heads in 57 us against 34: too few loads in flight.) Writing, four lanes own a block of 32
+// values, eight each: those whose codes share a word of the cache, so that no nibble changes
+// lanes and what a block needs once is done for eight blocks an instruction (eight lanes a block and
+// four values a lane: 19 us against 13 below). Reading, eight lanes own a block, four
+// neighbours each, and the dense side moves in coalesced 8- or 16-byte accesses. The codes follow the rule of q4_pack bit for bit: every binary32 step is an explicit
 // round-to-nearest operation. Measured on a B200: 8192 bfloat16 tokens of 8 heads of 128
-// written in 20 us (43 MB), 32768 read back as bfloat16 in 30 us (172 MB, 5.8 TB/s), as
+// written in 13 us (43 MB; 65536 in 85 us, 4.1 TB/s), 32768 read back as bfloat16 in 30 us (172 MB, 5.8 TB/s), as
 // binary32 in 51 us (306 MB, 6.0 TB/s, the copy rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -25,7 +27,6 @@ namespace q4kv {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kUnroll = 4;  // tokens (dim 64: pairs of tokens) of a run whose loads fly together
 constexpr uint32_t kFull = 0xffffffffu;
 
 // The warp's head, sequence and how many runs its own lies behind the sequence's first;
@@ -55,10 +56,28 @@ __device__ __forceinline__ uint8_t* record(const MoveParams& P, int s, int h, in
     return P.cache.data + record_at(P.cache, DIM, page, h, p - pg * P.cache.page_size);
 }
 
-__device__ __forceinline__ uint32_t max8(uint32_t v) {
-#pragma unroll
-    for (int off = 1; off < 8; off <<= 1) v = max(v, __shfl_xor_sync(kFull, v, off));
-    return v;
+// The largest over a block's four lanes.
+__device__ __forceinline__ uint32_t max4(uint32_t v) {
+    v = max(v, __shfl_xor_sync(kFull, v, 1));
+    return max(v, __shfl_xor_sync(kFull, v, 2));
+}
+
+// Two binary32 sums in one instruction, each rounded to nearest (add_rz: towards zero). (Their
+// products are single operations: packed ones were fused with the sum and rounded once.)
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_rn(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_rz(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // The code of one value: min(15, floor(t)) of t = v * inv + 8.5, as q4_pack rounds it. The
@@ -66,96 +85,101 @@ __device__ __forceinline__ uint32_t max8(uint32_t v) {
 __device__ __forceinline__ uint32_t code_slow(float v, float inv) {
     return (uint32_t)min(max((int)floorf(__fadd_rn(__fmul_rn(v, inv), 8.5f)), 0), 15);
 }
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
 
-// Quantises the eight lanes' 32 values: *word = word i8 % 4 of the block's codes (in
-// lanes i8 and i8 ^ 4), *d = its scale (in every lane). A block that holds a NaN or an
+// Quantises a block's 32 values, of which lane c of its four holds 4c .. 4c + 3 and 16 + 4c ..:
+// *word = word c of its codes, *d = its scale (in every lane). A block that holds a NaN or an
 // infinity gets the scale NaN. NARROW: the values come from 16-bit types, so that the low 13
 // bits of their binary32 are 0.
 template <bool NARROW>
-__device__ __forceinline__ void quantise(const float (&v)[4], int i8, uint32_t* word, uint16_t* d) {
+__device__ __forceinline__ void quantise(const float (&v)[8], int c, uint32_t* word, uint16_t* d) {
     // the value of largest magnitude, the lowest index of equal ones: the largest of
     // (magnitude, -index, sign), in one word where there is room for all three
-    uint32_t x[4], top, sign;
+    auto index = [](int j) { return j < 4 ? j : j + 12; };  // less 4c
+    uint32_t x[8], top, sign;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = __float_as_uint(v[j]);
+    for (int j = 0; j < 8; ++j) x[j] = __float_as_uint(v[j]);
     if constexpr (NARROW) {
         uint32_t key = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) key = max(key, ((x[j] & 0x7fffff80u) | (uint32_t)(62 - 8 * i8 - 2 * j)) + (x[j] >> 31));
-        key = max8(key);
+        for (int j = 0; j < 8; ++j) key = max(key, ((x[j] & 0x7fffff80u) | (uint32_t)(62 - 8 * c - 2 * index(j))) + (x[j] >> 31));
+        key = max4(key);
         top = key & 0x7fffff80u;
         sign = key << 31;
     } else {
         top = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, x[j] & 0x7fffffffu);
-        top = max8(top);
+        for (int j = 0; j < 8; ++j) top = max(top, x[j] & 0x7fffffffu);
+        top = max4(top);
         uint32_t key = 0;
 #pragma unroll
-        for (int j = 3; j >= 0; --j)
-            if ((x[j] & 0x7fffffffu) == top) key = (uint32_t)(64 - 8 * i8 - 2 * j) + (x[j] >> 31);
-        sign = max8(key) << 31;
+        for (int j = 7; j >= 0; --j)
+            if ((x[j] & 0x7fffffffu) == top) key = (uint32_t)(64 - 8 * c - 2 * index(j)) + (x[j] >> 31);
+        sign = max4(key) << 31;
     }
     if (top == 0) sign = 0;  // the rule starts from +0
     const float dd = __fmul_rn(__uint_as_float(top | sign), -0.125f);  // m / -8
     const float inv = dd != 0.0f ? __frcp_rn(dd) : 0.0f;
-    // t is 0.5 or more: 2^23 + t rounded towards zero has floor(t) in its low bits. Not so where
-    // 1 / d overflows (|d| < 2^-127).
-    uint32_t q[4];
-    if (__any_sync(kFull, fabsf(inv) > 0x1p126f)) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = code_slow(v[j], inv);
+    uint32_t lo, hi;  // bytes: the codes of the first four values, of the last four
+    if (__any_sync(kFull, fabsf(inv) > 0x1p126f)) {  // where 1 / d overflows (|d| < 2^-127), and near it
+        lo = low_bytes(code_slow(v[0], inv), code_slow(v[1], inv), code_slow(v[2], inv), code_slow(v[3], inv));
+        hi = low_bytes(code_slow(v[4], inv), code_slow(v[5], inv), code_slow(v[6], inv), code_slow(v[7], inv));
     } else {
+        // t is 0.5 or more: 2^23 + t rounded towards zero has floor(t), 0 .. 16, in its low bits
+        uint64_t q[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            q[j] = (uint32_t)min(__float_as_int(__fadd_rz(__fadd_rn(__fmul_rn(v[j], inv), 8.5f), 0x1p23f)), 0x4b00000f);
+            q[j] = add_rz(add_rn(two(__fmul_rn(v[2 * j], inv), __fmul_rn(v[2 * j + 1], inv)), two(8.5f, 8.5f)), two(0x1p23f, 0x1p23f));
+        lo = low_bytes((uint32_t)q[0], (uint32_t)(q[0] >> 32), (uint32_t)q[1], (uint32_t)(q[1] >> 32));
+        hi = low_bytes((uint32_t)q[2], (uint32_t)(q[2] >> 32), (uint32_t)q[3], (uint32_t)(q[3] >> 32));
+        lo -= lo >> 4 & 0x01010101u, hi -= hi >> 4 & 0x01010101u;  // 16 to 15
     }
-    const uint32_t w = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
-    const uint32_t o = __shfl_xor_sync(kFull, w, 4);
-    *word = (i8 < 4 ? o : w) * 16 + (i8 < 4 ? w : o);
+    *word = lo + hi * 16;
     *d = top >= 0x7f800000u ? (uint16_t)0x7fffu : __half_as_ushort(__float2half_rn(dd));
 }
 
-// Where the lane's parts of a token go: for the chunk that holds block bb.
+// Where the lane's parts of a token go in the first chunk: its word of the keys, a half of its
+// values and its neighbour block's, and a scale (lane c 0: the key's, 1: the value's).
 struct WriteAt {
-    uint8_t *key, *key_d, *value, *value_d;
+    uint8_t *key, *value, *scale;
 };
+template <int DIM>
+__device__ __forceinline__ WriteAt write_at(uint8_t* rec, int t, int bb, int c) {
+    return {rec + key_word(DIM, t, bb, c), rec + value_half(DIM, t, bb & ~1, 2 * c + (bb & 1)),
+            rec + (c == 0 ? key_scale(DIM, t, bb) : value_scale(DIM, t, bb))};
+}
 
-// Quantises the lane's four values of each chunk's key and value and stores them; not `mine`:
+// Quantises the lane's eight values of each chunk's key and value and stores them; not `mine`:
 // takes part only.
 template <int DIM, int T>
-__device__ __forceinline__ void write_token(const WriteAt& to, const float (&v)[DIM / 32 / chunk_blocks(DIM)][2][4], int bb, int i8,
+__device__ __forceinline__ void write_token(const WriteAt& to, const float (&v)[DIM / 32 / chunk_blocks(DIM)][2][8], int bb, int c,
                                             bool mine) {
     constexpr int C = chunk_blocks(DIM), NCH = DIM / 32 / C;
     constexpr bool NARROW = T == Q4_F16 || T == Q4_BF16;
-    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int ch = 0; ch < NCH; ++ch) {
-        uint32_t word;
-        uint16_t d;
-        quantise<NARROW>(v[ch][0], i8, &word, &d);
-        const int next_key = key_word(DIM, 0, ch * C, 0) - key_word(DIM, 0, 0, 0);
-        if (mine && i8 < 4) *reinterpret_cast<uint32_t*>(to.key + next_key) = word;
-        if (mine && i8 == 0) *reinterpret_cast<uint16_t*>(to.key_d + 2 * ch * C) = d;
-        quantise<NARROW>(v[ch][1], i8, &word, &d);
-        // lane i8 takes half i8 of its block; the halves i8 of the chunk's blocks are neighbours
-        const uint32_t w = __shfl_sync(kFull, word, (lane & 24) + (i8 >> 1));
-        const uint32_t half = i8 & 1 ? w >> 16 : w;
-        const uint32_t pair = __byte_perm(half, __shfl_xor_sync(kFull, half, 8), 0x5410);
-        uint8_t* const value = to.value + (value_half(DIM, 0, ch * C, 0) - value_half(DIM, 0, 0, 0));
-        if (C == 2) {
-            if (mine && bb == 0) *reinterpret_cast<uint32_t*>(value) = pair;
-        } else {
-            const uint32_t next = __shfl_xor_sync(kFull, pair, 16);
-            if (mine && bb == 0) *reinterpret_cast<uint2*>(value) = make_uint2(pair, next);
+        uint32_t key, word;
+        uint16_t key_d, value_d;
+        quantise<NARROW>(v[ch][0], c, &key, &key_d);
+        quantise<NARROW>(v[ch][1], c, &word, &value_d);
+        // the same half of neighbouring blocks are neighbours: the even block's lane takes half
+        // 2c of both, the odd one's half 2c + 1
+        const uint32_t pair = __byte_perm(word, __shfl_xor_sync(kFull, word, 4), bb & 1 ? 0x3276 : 0x5410);
+        if (mine) {
+            *reinterpret_cast<uint32_t*>(to.key + (key_word(DIM, 0, ch * C, 0) - key_word(DIM, 0, 0, 0))) = key;
+            *reinterpret_cast<uint32_t*>(to.value + (value_half(DIM, 0, ch * C, 0) - value_half(DIM, 0, 0, 0))) = pair;
+            if (c < 2) *reinterpret_cast<uint16_t*>(to.scale + 2 * ch * C) = c == 0 ? key_d : value_d;
         }
-        if (mine && i8 == 0) *reinterpret_cast<uint16_t*>(to.value_d + 2 * ch * C) = d;
     }
 }
 
 template <int DIM, int T>
 __global__ void __launch_bounds__(32 * kWarps) kv_write_kernel(const __grid_constant__ MoveParams P) {
-    constexpr int NB = DIM / 32, C = chunk_blocks(DIM), NCH = NB / C, L = 8 * C, TOK = 32 / L;  // TOK tokens at once
+    constexpr int NB = DIM / 32, C = chunk_blocks(DIM), NCH = NB / C, L = 4 * C, TOK = 32 / L;  // TOK tokens at once
+    constexpr int STEPS = kRun / TOK, FLY = STEPS * NCH <= 4 ? STEPS : 4 / NCH;  // steps of a run; those whose loads fly together
     Task k;
     if (!task_of(P, &k)) return;
     const int len = P.seqs.lens[k.s];
@@ -167,47 +191,45 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_kernel(const __grid_cons
     if (n <= 0) return;
     uint8_t* const at = record<DIM>(P, k.s, k.h, run);
     if (!at) return;
-    const int lane = threadIdx.x & 31, sub = lane / L, bb = lane % L / 8, i8 = lane & 7;
+    const int lane = threadIdx.x & 31, sub = lane / L, bb = lane % L / 4, c = lane & 3;
     const int t0 = (int)(p0 % kGroup), i0 = (int)(p0 - first);
-    const int64_t ks = row_at(P.k, k.s, i0, k.h) + bb * 32 + 4 * i8, vs = row_at(P.v, k.s, i0, k.h) + bb * 32 + 4 * i8;
+    const int64_t ks = row_at(P.k, k.s, i0, k.h) + bb * 32 + 4 * c, vs = row_at(P.v, k.s, i0, k.h) + bb * 32 + 4 * c;
+    auto load = [&](int i, float(&v)[NCH][2][8]) {  // the lane's values of the run's token i
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float x[4], y[4];
+                load_four<T>(P.k, ks + i * P.k.token + ch * 32 * C + 16 * half, x);
+                load_four<T>(P.v, vs + i * P.v.token + ch * 32 * C + 16 * half, y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[ch][0][4 * half + j] = x[j], v[ch][1][4 * half + j] = y[j];
+            }
+    };
     if (n == kRun) {
         // a whole run, aligned in its record: every place is known but for the lane's own
-        const WriteAt to = {at + key_word(DIM, t0, bb, i8 & 3), at + key_scale(DIM, t0, bb), at + value_half(DIM, t0, bb, i8),
-                            at + value_scale(DIM, t0, bb)};
+        const WriteAt to = write_at<DIM>(at, t0 + sub, bb, c);
 #pragma unroll
-        for (int half = 0; half < kRun / TOK; half += kUnroll) {
-            float v[kUnroll][NCH][2][4];
+        for (int step = 0; step < STEPS; step += FLY) {
+            float v[FLY][NCH][2][8];
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i)
+            for (int i = 0; i < FLY; ++i) load((step + i) * TOK + sub, v[i]);
 #pragma unroll
-                for (int ch = 0; ch < NCH; ++ch) {
-                    load_four<T>(P.k, ks + ((half + i) * TOK + sub) * P.k.token + ch * 32 * C, v[i][ch][0]);
-                    load_four<T>(P.v, vs + ((half + i) * TOK + sub) * P.v.token + ch * 32 * C, v[i][ch][1]);
-                }
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                // token t of an aligned run of eight (TOK 2: the second half warp's is odd)
-                const int t = (half + i) * TOK;
-                const WriteAt at_t = {to.key + (key_word(DIM, t, 0, 0) - key_word(DIM, 0, 0, 0)) + sub * 16 * C,
-                                      to.key_d + t * 2 * NB + sub * 2 * NB,
-                                      to.value + (value_half(DIM, t, 0, 0) - value_half(DIM, 0, 0, 0)) + sub * 2 * C,
-                                      to.value_d + t * 2 * NB + sub * 2 * NB};
-                write_token<DIM, T>(at_t, v[i], bb, i8, true);
+            for (int i = 0; i < FLY; ++i) {
+                const int t = (step + i) * TOK;
+                const WriteAt at_t = {to.key + (key_word(DIM, t, 0, 0) - key_word(DIM, 0, 0, 0)),
+                                      to.value + (value_half(DIM, t, 0, 0) - value_half(DIM, 0, 0, 0)), to.scale + t * 2 * NB};
+                write_token<DIM, T>(at_t, v[i], bb, c, true);
             }
         }
     } else {
+#pragma unroll 1
         for (int base = 0; base < n; base += TOK) {
             const bool mine = base + sub < n;
-            const int i = mine ? base + sub : n - 1, t = t0 + i;  // the last token twice rather than none
-            float v[NCH][2][4];
-#pragma unroll
-            for (int ch = 0; ch < NCH; ++ch) {
-                load_four<T>(P.k, ks + i * P.k.token + ch * 32 * C, v[ch][0]);
-                load_four<T>(P.v, vs + i * P.v.token + ch * 32 * C, v[ch][1]);
-            }
-            const WriteAt at_t = {at + key_word(DIM, t, bb, i8 & 3), at + key_scale(DIM, t, bb), at + value_half(DIM, t, bb, i8),
-                                  at + value_scale(DIM, t, bb)};
-            write_token<DIM, T>(at_t, v, bb, i8, mine);
+            const int i = mine ? base + sub : n - 1;  // the last token twice rather than none
+            float v[NCH][2][8];
+            load(i, v);
+            write_token<DIM, T>(write_at<DIM>(at, t0 + i, bb, c), v, bb, c, mine);
         }
     }
 }
