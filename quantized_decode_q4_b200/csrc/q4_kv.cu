@@ -62,6 +62,18 @@ __device__ __forceinline__ uint32_t max4(uint32_t v) {
     return max(v, __shfl_xor_sync(kFull, v, 2));
 }
 
+// The larger and the smaller, NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Two binary32 sums in one instruction, each rounded to nearest (add_rz: towards zero). (Their
 // products are single operations: packed ones were fused with the sum and rounded once.)
 __device__ __forceinline__ uint64_t two(float a, float b) {
@@ -92,36 +104,30 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
 
 // Quantises a block's 32 values, of which lane c of its four holds 4c .. 4c + 3 and 16 + 4c ..:
 // *word = word c of its codes, *d = its scale (in every lane). A block that holds a NaN or an
-// infinity gets the scale NaN. NARROW: the values come from 16-bit types, so that the low 13
-// bits of their binary32 are 0.
-template <bool NARROW>
+// infinity gets the scale NaN.
 __device__ __forceinline__ void quantise(const float (&v)[8], int c, uint32_t* word, uint16_t* d) {
-    // the value of largest magnitude, the lowest index of equal ones: the largest of
-    // (magnitude, -index, sign), in one word where there is room for all three
-    auto index = [](int j) { return j < 4 ? j : j + 12; };  // less 4c
-    uint32_t x[8], top, sign;
+    // the value of largest magnitude, the lowest index of equal ones: the largest or the
+    // smallest value, NaN where one is
+    float most = v[0], least = v[0];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __float_as_uint(v[j]);
-    if constexpr (NARROW) {
-        uint32_t key = 0;
+    for (int j = 1; j < 8; ++j) most = max_nan(most, v[j]), least = min_nan(least, v[j]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) key = max(key, ((x[j] & 0x7fffff80u) | (uint32_t)(62 - 8 * c - 2 * index(j))) + (x[j] >> 31));
-        key = max4(key);
-        top = key & 0x7fffff80u;
-        sign = key << 31;
-    } else {
-        top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, x[j] & 0x7fffffffu);
-        top = max4(top);
-        uint32_t key = 0;
+    for (int off = 1; off < 4; off <<= 1) {
+        most = max_nan(most, __shfl_xor_sync(kFull, most, off));
+        least = min_nan(least, __shfl_xor_sync(kFull, least, off));
+    }
+    float m = most > -least ? most : least;
+    if (__any_sync(kFull, most == -least && most != 0.0f)) {
+        // as large on both sides: the first of them
+        uint32_t key = 0;  // (32 - index, sign)
 #pragma unroll
         for (int j = 7; j >= 0; --j)
-            if ((x[j] & 0x7fffffffu) == top) key = (uint32_t)(64 - 8 * c - 2 * index(j)) + (x[j] >> 31);
-        sign = max4(key) << 31;
+            if (fabsf(v[j]) == most) key = (uint32_t)(64 - 8 * c - 2 * (j < 4 ? j : j + 12)) + (__float_as_uint(v[j]) >> 31);
+        key = max4(key);
+        if (most == -least) m = key & 1 ? least : most;
     }
-    if (top == 0) sign = 0;  // the rule starts from +0
-    const float dd = __fmul_rn(__uint_as_float(top | sign), -0.125f);  // m / -8
+    m = __fadd_rn(m, 0.0f);  // the rule starts from +0
+    const float dd = __fmul_rn(m, -0.125f);  // m / -8
     const float inv = dd != 0.0f ? __frcp_rn(dd) : 0.0f;
     uint32_t lo, hi;  // bytes: the codes of the first four values, of the last four
     if (__any_sync(kFull, fabsf(inv) > 0x1p126f)) {  // where 1 / d overflows (|d| < 2^-127), and near it
@@ -138,7 +144,7 @@ __device__ __forceinline__ void quantise(const float (&v)[8], int c, uint32_t* w
         lo -= lo >> 4 & 0x01010101u, hi -= hi >> 4 & 0x01010101u;  // 16 to 15
     }
     *word = lo + hi * 16;
-    *d = top >= 0x7f800000u ? (uint16_t)0x7fffu : __half_as_ushort(__float2half_rn(dd));
+    *d = !(fabsf(m) < INFINITY) ? (uint16_t)0x7fffu : __half_as_ushort(__float2half_rn(dd));
 }
 
 // Where the lane's parts of a token go in the first chunk: its word of the keys, a half of its
@@ -154,17 +160,16 @@ __device__ __forceinline__ WriteAt write_at(uint8_t* rec, int t, int bb, int c) 
 
 // Quantises the lane's eight values of each chunk's key and value and stores them; not `mine`:
 // takes part only.
-template <int DIM, int T>
+template <int DIM>
 __device__ __forceinline__ void write_token(const WriteAt& to, const float (&v)[DIM / 32 / chunk_blocks(DIM)][2][8], int bb, int c,
                                             bool mine) {
     constexpr int C = chunk_blocks(DIM), NCH = DIM / 32 / C;
-    constexpr bool NARROW = T == Q4_F16 || T == Q4_BF16;
 #pragma unroll
     for (int ch = 0; ch < NCH; ++ch) {
         uint32_t key, word;
         uint16_t key_d, value_d;
-        quantise<NARROW>(v[ch][0], c, &key, &key_d);
-        quantise<NARROW>(v[ch][1], c, &word, &value_d);
+        quantise(v[ch][0], c, &key, &key_d);
+        quantise(v[ch][1], c, &word, &value_d);
         // the same half of neighbouring blocks are neighbours: the even block's lane takes half
         // 2c of both, the odd one's half 2c + 1
         const uint32_t pair = __byte_perm(word, __shfl_xor_sync(kFull, word, 4), bb & 1 ? 0x3276 : 0x5410);
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_kernel(const __grid_cons
                 const int t = (step + i) * TOK;
                 const WriteAt at_t = {to.key + (key_word(DIM, t, 0, 0) - key_word(DIM, 0, 0, 0)),
                                       to.value + (value_half(DIM, t, 0, 0) - value_half(DIM, 0, 0, 0)), to.scale + t * 2 * NB};
-                write_token<DIM, T>(at_t, v[i], bb, c, true);
+                write_token<DIM>(at_t, v[i], bb, c, true);
             }
         }
     } else {
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_write_kernel(const __grid_cons
             const int i = mine ? base + sub : n - 1;  // the last token twice rather than none
             float v[NCH][2][8];
             load(i, v);
-            write_token<DIM, T>(write_at<DIM>(at, t0 + i, bb, c), v, bb, c, mine);
+            write_token<DIM>(write_at<DIM>(at, t0 + i, bb, c), v, bb, c, mine);
         }
     }
 }
