@@ -91,6 +91,9 @@ q4_status q4_debug_gemv_stall(const q4_matrix* m, const float* X, int b, float* 
  * the first failed check. */
 int q4_debug_check_kv_layout(int dim);
 
+/* n / d as q4_kv_write and q4_kv_read divide: n >= 0, d >= 1. */
+int32_t q4_debug_kv_quotient(int32_t n, int32_t d);
+
 /* Replay of q4_kv_attention's division of work for `count` sequences (lens, new_lens or
  * NULL), `units` units a sequence, a table that reaches table_tokens positions, on `grid`
  * CTAs of `warps` warps: spans cover what is seen, CTA and warp ranges cover every tile once,

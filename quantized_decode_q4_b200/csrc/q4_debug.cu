@@ -604,6 +604,8 @@ int64_t q4_debug_check_unpack(uint64_t seed, int64_t count) {
     return bad;
 }
 
+int32_t q4_debug_kv_quotient(int32_t n, int32_t d) { return q4kv::divisor(d).of(n); }
+
 int q4_debug_check_kv_layout(int dim) {
     using namespace q4kv;
     if (dim != 64 && dim != 128 && dim != 256) return 1;

@@ -7,11 +7,12 @@
 // heads in 57 us against 34: too few loads in flight.) Writing, four lanes own a block of 32
 // values, eight each: those whose codes share a word of the cache, so that no nibble changes
 // lanes and what a block needs once is done for eight blocks an instruction (eight lanes a block and
-// four values a lane: 19 us against 13 below). Reading, eight lanes own a block, four
-// neighbours each, and the dense side moves in coalesced 8- or 16-byte accesses. The codes follow the rule of q4_pack bit for bit: every binary32 step is an explicit
-// round-to-nearest operation. Measured on a B200: 8192 bfloat16 tokens of 8 heads of 128
-// written in 13 us (43 MB; 65536 in 85 us, 4.1 TB/s), 32768 read back as bfloat16 in 30 us (172 MB, 5.8 TB/s), as
-// binary32 in 51 us (306 MB, 6.0 TB/s, the copy rate).
+// four values a lane: 19 us against 13). Reading, eight lanes own a block, four neighbours
+// each. Either way the dense side moves in coalesced 8- or 16-byte accesses, and the codes
+// follow the rule of q4_pack bit for bit: every binary32 step is an explicit round-to-nearest
+// operation. Measured on a B200: 8192 bfloat16 tokens of 8 heads of 128 written in 12 us (43 MB;
+// 65536 in 78 us, 4.4 TB/s, about 125 instructions a token and head), 32768 read back as
+// bfloat16 in 30 us (172 MB, 5.8 TB/s), as binary32 in 51 us (306 MB, 6.1 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -35,13 +36,12 @@ struct Task {
     int s, r, h;
 };
 __device__ __forceinline__ bool task_of(const MoveParams& P, Task* t) {
-    uint32_t n = blockIdx.x * (uint32_t)kWarps + (threadIdx.x >> 5);
+    const uint32_t n = blockIdx.x * (uint32_t)kWarps + (threadIdx.x >> 5);
     if (n >= (uint32_t)P.items) return false;
-    const uint32_t heads = (uint32_t)P.cache.heads, runs = (uint32_t)P.runs;
-    t->h = (int)(n % heads);
-    n /= heads;
-    t->r = (int)(n % runs);
-    t->s = (int)(n / runs);
+    const int run = P.by_heads.of((int)n);
+    t->h = (int)n - run * P.cache.heads;
+    t->s = P.by_runs.of(run);
+    t->r = run - t->s * P.runs;
     return true;
 }
 
@@ -50,7 +50,7 @@ __device__ __forceinline__ bool task_of(const MoveParams& P, Task* t) {
 template <int DIM>
 __device__ __forceinline__ uint8_t* record(const MoveParams& P, int s, int h, int64_t run) {
     if (run < 0 || run >= reach(P.cache, P.seqs) / kRun) return nullptr;
-    const int p = (int)run * kRun, pg = p / P.cache.page_size;
+    const int p = (int)run * kRun, pg = P.by_page.of(p);
     const int page = P.seqs.table[s * P.seqs.table_stride + pg];
     if (page < 0 || page >= P.cache.pages) return nullptr;
     return P.cache.data + record_at(P.cache, DIM, page, h, p - pg * P.cache.page_size);

@@ -90,6 +90,9 @@ q4_status move_call(bool write, const q4_kv_cache* cache, const q4_kv_seqs* seqs
     P.tokens = tokens;
     P.runs = (int32_t)runs;
     P.items = (int32_t)(seqs->count * runs * cache->heads);
+    P.by_heads = q4kv::divisor(cache->heads);
+    P.by_runs = q4kv::divisor(P.runs);
+    P.by_page = q4kv::divisor(cache->page_size);
     if (cuda_failed(q4kv::launch_kv_move(write, cache->dim, P, static_cast<cudaStream_t>(stream)))) return Q4_ERR_CUDA;
     count_launches(1);
     return Q4_OK;

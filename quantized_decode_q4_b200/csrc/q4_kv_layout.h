@@ -79,6 +79,18 @@ struct Rows {  // [seqs][tokens][heads][dim], strides in elements
     int32_t vec;   // four neighbouring elements can be moved at once
 };
 
+// n / d for 0 <= n < 2^31 as a product, d in 1 .. 2^31 - 1: with m = ceil(2^(31 + l) / d), 2^l >= d, the
+// product n * m is above 2^(31 + l) * n / d by less than 2^(31 + l) / d.
+struct Divisor {
+    uint32_t m, shift;
+    __host__ __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+inline Divisor divisor(int32_t d) {
+    uint32_t l = 0;
+    while ((INT64_C(1) << l) < d) ++l;
+    return {(uint32_t)(((UINT64_C(1) << (31 + l)) + d - 1) / d), 31 + l};
+}
+
 struct MoveParams {  // write and read
     Cache cache;
     Seqs seqs;
@@ -87,6 +99,7 @@ struct MoveParams {  // write and read
     int32_t tokens;
     int32_t runs;   // of kRun positions that `tokens` positions touch at most
     int32_t items;  // seqs * runs * heads
+    Divisor by_heads, by_runs, by_page;
 };
 
 struct AttnParams {

@@ -1,6 +1,7 @@
 """The 4-bit key/value cache on the CPU: sizes, refusals before any CUDA call, and the
 record layout."""
 import ctypes
+import random
 
 import numpy as np
 import pytest
@@ -171,3 +172,15 @@ def test_packed_arguments_are_the_structure():
         assert call(which, null=True) == INVALID and call(which, tokens=0) == 0
         assert call(which, c=(256, 0, 2, 64, 32)) == INVALID and call(which, c=(192, 4, 2, 64, 32)) == MISALIGNED
     assert call(2, tokens=17) == UNSUPPORTED and call(2, ws=0) == WORKSPACE and call(3) == INVALID and call(-1) == INVALID
+
+
+def test_quotients():
+    f = q4.lib().q4_debug_kv_quotient
+    top = 2**31 - 1
+    g = random.Random(3)
+    divisors = [1, 2, 3, 5, 7, 8, 32, 96, 127, 128, 65535, 65536, 2**30 - 1, 2**30, 2**30 + 1, top - 1, top]
+    for d in divisors + [int(2**g.uniform(0, 31)) for _ in range(200)]:
+        near = [m * d + e for m in (1, 2, top // d // 2, top // d) for e in (-1, 0, 1)]
+        for n in [0, 1, top - 1, top] + near + [g.randrange(2**31) for _ in range(20)]:
+            if 0 <= n <= top:
+                assert f(n, d) == n // d, (n, d)
