@@ -48,7 +48,7 @@
 //
 // Measured on a B200 (device time): 16 sequences of up to 32768 tokens, 32 query heads on 8
 // of 128, bfloat16: 66 us, 285 MB, 4.3 TB/s (67% of the measured copy rate; the same with every
-// byte in L2: 64 us; without the products: 56 us); in binary32 75 us. 580 instructions a record, of
+// byte in L2: 64 us; without the products: 56 us); in binary32 76 us. 580 instructions a record, of
 // which 192 unpack, 80 are products, 64 apply key scales. One sequence of 8192 tokens: 12 us;
 // of 777, 3 heads of 64: 9 us. Per launch: about 2 us to find a warp's work and its page,
 // 1 us to lay the queries out, 4 us to join what warps and CTAs cut.
@@ -720,7 +720,7 @@ struct Producer {
         held.page = page, held.base = base, held.unit_left = unit - run;
     }
     __device__ __forceinline__ void seek(const AttnParams& P, volatile Held& held, const Place& at, int lane) {
-        const int tile = at.sp.tile0 + at.t, page = (int)((uint32_t)tile / (uint32_t)P.rpp);
+        const int tile = at.sp.tile0 + at.t, page = P.by_rpp.of(tile);
         put(held.next, at);
         load_entries(P, at.s, page, lane);
         open(P, held, at, page, page, tile - page * P.rpp, at.sp.n - at.t, lane);
@@ -913,7 +913,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
         // the place of tile wa
         {
             Place at;
-            const int y = (int)((uint32_t)wa / (uint32_t)P.units);
+            const int y = P.by_units.of(wa);
             int rest;
             if (few) {
                 at.s = 31 - __clz(__ballot_sync(kFull, before <= y && lane < P.seqs.count));
@@ -944,7 +944,7 @@ __global__ void __launch_bounds__(F::THREADS, 1) kv_attention_kernel(const __gri
             const int off = wa - (y - rest) * P.units, u = (int)((uint32_t)off / (uint32_t)at.sp.n);
             at.t = off - u * at.sp.n;
             at.h = u, at.rt = 0;
-            if (P.rt_count > 1) at.h = (int)((uint32_t)u / (uint32_t)P.rt_count), at.rt = u - at.h * P.rt_count;
+            if (P.rt_count > 1) at.h = P.by_rt.of(u), at.rt = u - at.h * P.rt_count;
             held.start = wa - at.t;
             put(held.at, at);
         }
@@ -1171,6 +1171,7 @@ template <class F>
 cudaError_t run(AttnParams P, int num_sms, cudaStream_t stream) {
     P.rt_count = (P.rows + F::RC - 1) / F::RC;
     P.units = P.cache.heads * P.rt_count;
+    P.by_rpp = divisor(P.rpp), P.by_rt = divisor(P.rt_count), P.by_units = divisor(P.units);
     if (P.window > kNoWindow) P.window = 0;
     const int grid = num_sms < kMaxCtas ? num_sms : kMaxCtas;
     kv_attention_kernel<F><<<grid, F::THREADS, F::SMEM, stream>>>(P);

@@ -117,6 +117,7 @@ struct AttnParams {
     int32_t rpp;           // records of a page
     uint32_t tx_extra;     // 0; a test's waits expect so many bytes more than come
     int32_t rt_count, units;  // row tiles of a key/value head, units of a sequence: set at the launch
+    Divisor by_rpp, by_rt, by_units;
 };
 
 }  // namespace q4kv
